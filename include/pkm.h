@@ -388,6 +388,117 @@ pkm_status pkm_shard_value_grad(const pkm_dims* d, int32_t G, int64_t shard_rows
 pkm_status pkm_shard_scatter_dw(const pkm_dims* d, const int32_t* perm, const float* dw_ret,
                                 float* dw, void* stream);
 
+/* ---------------------------------------------------------------- gated feed-forward block
+ * The block a memory layer stands beside or replaces in a transformer ("Large Memory Layers
+ * with Product Keys" puts the memory in the place of some feed-forward blocks):
+ *     g = x Wg^T,  u = x Wu^T,  h = act(g) * u,  y = h Wd^T.
+ * Row-major layouts, storage type T = bf16 (fp32 with PKM_F_FP32):
+ *     x [N][d_in]   Wg, Wu [d_ff][d_in]   Wd [d_out][d_ff]   y, dy [N][d_out]   dx [N][d_in]
+ * d_in, d_ff and d_out are multiples of 8.  N == 0 is a no-op returning PKM_OK.
+ * Products are accumulated in fp32.  With bf16 storage on tensor cores h, dg and du are
+ * rounded to bf16 before the product that takes them; with PKM_F_FP32 or PKM_F_SIMT they
+ * stay fp32.  flags: PKM_F_FP32, PKM_F_SIMT and the PKM_FFN_* below. */
+#define PKM_ACT_SILU 0 /* v / (1 + exp(-v)) */
+#define PKM_ACT_GELU 1 /* v Phi(v), Phi the normal distribution function (no approximation) */
+
+/* The projections are kept for the backward as 8-bit activation checkpoints
+ * (pkm_ckpt8_pack) of their fp32 values, instead of in the storage type. */
+#define PKM_FFN_CKPT8 0x100u
+/* Weight gradients are bf16 and OVERWRITTEN (a step of one backward), instead of fp32 and
+ * accumulated (+=).  bf16 storage only. */
+#define PKM_FFN_GRAD_BF16 0x200u
+
+typedef struct {
+  int64_t N;      /* tokens */
+  int32_t d_in;   /* input width */
+  int32_t d_ff;   /* inner width */
+  int32_t d_out;  /* output width */
+  int32_t act;    /* PKM_ACT_* */
+  uint32_t flags;
+} pkm_ffn_dims;
+
+/* What the forward keeps for the backward (caller-owned; the backward needs x too).
+ *   g, u              [N][d_ff] in the storage type, or with PKM_FFN_CKPT8 the int8 codes
+ *                     [N][32 * ceil(d_ff / 32)]
+ *   g_scale, u_scale  with PKM_FFN_CKPT8 the scales [N][ceil(d_ff / 32)] fp32; else unused */
+typedef struct {
+  void* g;
+  void* u;
+  float* g_scale;
+  float* u_scale;
+} pkm_ffn_saved;
+
+#define PKM_FFN_SAVED_G 0
+#define PKM_FFN_SAVED_U 1
+#define PKM_FFN_SAVED_G_SCALE 2
+#define PKM_FFN_SAVED_U_SCALE 3
+
+/* Bytes of one pkm_ffn_saved field (PKM_FFN_SAVED_*) for these dims; 0 for bad input. */
+size_t pkm_ffn_saved_bytes(const pkm_ffn_dims* d, int field);
+/* Bytes of workspace (256-byte aligned) of pkm_ffn_forward and pkm_w4_ffn (PKM_FWD) or
+ * pkm_ffn_backward (PKM_BWD).  Contents on entry are ignored, on return unspecified; calls
+ * whose work may overlap need workspaces of their own. */
+size_t pkm_ffn_workspace_bytes(const pkm_ffn_dims* d, int which);
+
+/* y is overwritten.  saved == NULL keeps nothing (evaluation, decoding). */
+pkm_status pkm_ffn_forward(const pkm_ffn_dims* d, const void* x, const void* Wg, const void* Wu,
+                           const void* Wd, void* y, const pkm_ffn_saved* saved, void* workspace,
+                           size_t workspace_bytes, void* stream);
+/* Gradients of sum_t dy[t] . y[t]:
+ *     dh = dy Wd, dg = dh * u * act'(g), du = dh * act(g),
+ *     dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dWd = dy^T h.
+ * dx [N][d_in] in the storage type, overwritten.  dWg, dWu [d_ff][d_in], dWd [d_out][d_ff]:
+ * fp32, +=, or bf16, overwritten, with PKM_FFN_GRAD_BF16.  A NULL gradient is skipped. */
+pkm_status pkm_ffn_backward(const pkm_ffn_dims* d, const void* x, const void* Wg, const void* Wu,
+                            const void* Wd, const pkm_ffn_saved* saved, const void* dy, void* dx,
+                            void* dWg, void* dWu, void* dWd, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* ---- 8-bit activation checkpoints ----
+ * Each run of 32 columns of a row (the last may be shorter) shares one scale: with
+ * top = max |a| over the run, scale = top / 127 (fp32), code = 127 a / top rounded to the
+ * nearest integer, halves to even; the value is code * scale.  A run that holds a NaN or an
+ * infinity gets scale NaN and codes 0, so every value of it reads as NaN.
+ *   src, dst [rows][cols] bf16 (fp32 with flags = PKM_F_FP32), cols a multiple of 8
+ *   codes    [rows][32 * ceil(cols / 32)] int8, zero behind the last column
+ *   scale    [rows][ceil(cols / 32)] fp32
+ * Used by pkm_ffn_forward / pkm_ffn_backward with PKM_FFN_CKPT8, and for any other activation
+ * a step has to keep (the layer's input x of pkm_query_grad, q-hat): pack after its last
+ * forward use, unpack before the backward. */
+pkm_status pkm_ckpt8_pack(int64_t rows, int32_t cols, uint32_t flags, const void* src,
+                          int8_t* codes, float* scale, void* stream);
+pkm_status pkm_ckpt8_unpack(int64_t rows, int32_t cols, uint32_t flags, const int8_t* codes,
+                            const float* scale, void* dst, void* stream);
+
+/* ---- products with 4-bit weights (decoding) ----
+ * W[o][i] = (code[o][i] - 8) * scale[o][i / group], code in 0 .. 15.
+ *   codes  [d_out][d_in / 2] bytes, column 2j in the low half of byte j, 2j + 1 in the high
+ *   scale  [d_out][ceil(d_in / group)] bf16
+ * d_in is a multiple of 32, group a multiple of 32 (the last group of a row may be shorter). */
+typedef struct {
+  const uint8_t* codes;
+  const void* scale;
+} pkm_w4;
+#define PKM_W4_MAX_TOKENS 64
+/* From a bf16 matrix: scale = bf16(max |w| / 7) over the group, code = w / scale rounded to
+ * the nearest integer (halves to even), held within -8 .. 7, plus 8.  A group that holds a
+ * NaN or an infinity gets scale NaN. */
+pkm_status pkm_w4_pack(int32_t d_out, int32_t d_in, int32_t group, const void* W, uint8_t* codes,
+                       void* scale, void* stream);
+/* The bf16 matrix the codes stand for, for calls of more tokens than PKM_W4_MAX_TOKENS. */
+pkm_status pkm_w4_unpack(int32_t d_out, int32_t d_in, int32_t group, const pkm_w4* W, void* out,
+                         void* stream);
+/* y [N][d_out] fp32 = x W^T, x [N][d_in] bf16, N <= PKM_W4_MAX_TOKENS (more:
+ * PKM_ERR_UNSUPPORTED).  The products are exact and their sums fp32. */
+pkm_status pkm_w4_matvec(int64_t N, int32_t d_in, int32_t d_out, int32_t group, const void* x,
+                         const pkm_w4* W, float* y, void* stream);
+/* The gated block with 4-bit weights: Wg, Wu [d_ff][d_in], Wd [d_out][d_ff]; x and y bf16,
+ * d->flags == 0, d_ff a multiple of 32, any d_out, N <= PKM_W4_MAX_TOKENS.  Workspace:
+ * pkm_ffn_workspace_bytes(d, PKM_FWD). */
+pkm_status pkm_w4_ffn(const pkm_ffn_dims* d, int32_t group, const void* x, const pkm_w4* Wg,
+                      const pkm_w4* Wu, const pkm_w4* Wd, void* y, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device status word of the
  * current device.  Returns PKM_OK, PKM_ERR_DEVICE_TIMEOUT, PKM_ERR_DEVICE_INDEX or
  * PKM_ERR_CUDA (when the synchronisation itself failed). */

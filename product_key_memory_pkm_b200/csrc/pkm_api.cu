@@ -42,6 +42,17 @@ bool device_setup(int* dev_out) {
   return true;
 }
 
+}  // namespace
+
+bool current_device(DeviceInfo* info) {
+  int dev = 0;
+  if (!device_setup(&dev)) return false;
+  *info = DeviceInfo{dev, g_sm_count[dev], g_status_ptr[dev]};
+  return true;
+}
+
+namespace {
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 pkm_status validate_dims(const pkm_dims* d) {

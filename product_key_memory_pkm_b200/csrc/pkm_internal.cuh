@@ -73,6 +73,15 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, si
 void count_launches(int n);
 #define PKM_COUNT(n) ::pkm::count_launches(n)
 
+// ---------------------------------------------------------------- device
+// The current device with its SM count and status word; false if a CUDA call failed.
+struct DeviceInfo {
+  int dev;
+  int sm_count;
+  int* status;
+};
+bool current_device(DeviceInfo* info);
+
 // ---------------------------------------------------------------- plan
 // Sizes derived once per call from pkm_dims.
 struct Plan {

@@ -38,6 +38,12 @@ PKM_FWD, PKM_BWD, PKM_FWD_FUSED = 0, 1, 2
 PKM_FW_LOOKAHEAD = 0x1
 PKM_FW_SORT_GLOBAL = 0x2
 PKM_FW_PER_CHUNK = 0x4
+PKM_ACT_SILU, PKM_ACT_GELU = 0, 1
+PKM_FFN_CKPT8 = 0x100
+PKM_FFN_GRAD_BF16 = 0x200
+PKM_W4_MAX_TOKENS = 64
+CKPT8_RUN = 32  # columns that share one scale of an 8-bit checkpoint
+FFN_SAVED_FIELDS = ("g", "u", "g_scale", "u_scale")
 SAVED_FIELDS = ("q", "qhat", "sub_s", "sub_i", "idx", "w", "bn_batch")
 PKM_MAX_SHARDS = 1024
 PKM_SHARD_ROUTE, PKM_SHARD_OWNER = 1, 2
@@ -51,7 +57,10 @@ EXPORTED = ("pkm_saved_bytes", "pkm_workspace_bytes", "pkm_forward", "pkm_backwa
             "pkm_fastweight_workspace_bytes", "pkm_fastweight_chunks", "pkm_value_sgd",
             "pkm_value_grad_rows", "pkm_value_adam", "pkm_hit_counts", "pkm_bn_running_update",
             "pkm_shard_workspace_bytes", "pkm_shard_route", "pkm_shard_bag", "pkm_shard_combine",
-            "pkm_shard_gather_dy", "pkm_shard_value_grad", "pkm_shard_scatter_dw")
+            "pkm_shard_gather_dy", "pkm_shard_value_grad", "pkm_shard_scatter_dw",
+            "pkm_ffn_saved_bytes", "pkm_ffn_workspace_bytes", "pkm_ffn_forward",
+            "pkm_ffn_backward", "pkm_ckpt8_pack", "pkm_ckpt8_unpack", "pkm_w4_pack",
+            "pkm_w4_unpack", "pkm_w4_matvec", "pkm_w4_ffn")
 
 
 class PKMError(RuntimeError):
@@ -71,6 +80,19 @@ class pkm_saved(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in SAVED_FIELDS]
 
 
+class pkm_ffn_dims(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("d_in", ctypes.c_int32), ("d_ff", ctypes.c_int32),
+                ("d_out", ctypes.c_int32), ("act", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class pkm_ffn_saved(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in FFN_SAVED_FIELDS]
+
+
+class pkm_w4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -86,6 +108,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     P, S, I, U64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint64
     D = ctypes.POINTER(pkm_dims)
     SV = ctypes.POINTER(pkm_saved)
+    FD, FS, W4 = (ctypes.POINTER(t) for t in (pkm_ffn_dims, pkm_ffn_saved, pkm_w4))
+    I64, I32, U32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32
     sig = {
         "pkm_saved_bytes": (S, [D, I]),
         "pkm_workspace_bytes": (S, [D, I]),
@@ -123,6 +147,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "pkm_shard_value_grad": (I, [D, ctypes.c_int32, ctypes.c_int64, P, ctypes.c_int64,
                                      ctypes.c_int64, P, P, P, P, P, P, S, P]),
         "pkm_shard_scatter_dw": (I, [D, P, P, P, P]),
+        "pkm_ffn_saved_bytes": (S, [FD, I]),
+        "pkm_ffn_workspace_bytes": (S, [FD, I]),
+        "pkm_ffn_forward": (I, [FD, P, P, P, P, P, FS, P, S, P]),
+        "pkm_ffn_backward": (I, [FD, P, P, P, P, FS, P, P, P, P, P, P, S, P]),
+        "pkm_ckpt8_pack": (I, [I64, I32, U32, P, P, P, P]),
+        "pkm_ckpt8_unpack": (I, [I64, I32, U32, P, P, P, P]),
+        "pkm_w4_pack": (I, [I32, I32, I32, P, P, P, P]),
+        "pkm_w4_unpack": (I, [I32, I32, I32, W4, P, P]),
+        "pkm_w4_matvec": (I, [I64, I32, I32, I32, P, W4, P, P]),
+        "pkm_w4_ffn": (I, [FD, I32, P, W4, W4, W4, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -470,3 +504,244 @@ def pkm_shard_value_grad(dims: Dims, G: int, shard_rows: int, recv_counts, n_tri
 def pkm_shard_scatter_dw(dims: Dims, perm, dw_ret, dw, stream=None) -> None:
     _check(load().pkm_shard_scatter_dw(ctypes.byref(dims.c()), _ptr(perm), _ptr(dw_ret), _ptr(dw),
                                        _stream(stream)), "pkm_shard_scatter_dw")
+
+
+# ------------------------------------------------------- gated feed-forward block
+# Unlike the raw-address calls above, these check the tensors they are given: type, shape,
+# contiguity and device (integer addresses pass unchecked).
+
+def _tensor(t, name: str, dtype, shape: tuple, optional: bool = False) -> int | None:
+    """Address of a contiguous ``shape`` tensor of ``dtype`` on the current device."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if isinstance(t, int):
+        return t
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} wanted, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {shape} wanted, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    _on_current(t, name)
+    return t.data_ptr()
+
+
+def _on_current(t, name: str) -> None:
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{name} is not on a GPU")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"{torch.cuda.current_device()}")
+
+
+def _ffn_workspace(workspace, workspace_bytes):
+    if workspace is not None and not isinstance(workspace, int):
+        if not workspace.is_contiguous():
+            raise ValueError("workspace is not contiguous")
+        _on_current(workspace, "workspace")
+    return _ptr(workspace), _ws(workspace, workspace_bytes)
+
+
+@dataclass(frozen=True)
+class FfnDims:
+    """Python mirror of ``pkm_ffn_dims``."""
+    N: int
+    d_in: int
+    d_ff: int
+    d_out: int
+    act: int = PKM_ACT_SILU
+    flags: int = 0
+
+    def c(self) -> pkm_ffn_dims:
+        return pkm_ffn_dims(self.N, self.d_in, self.d_ff, self.d_out, self.act, self.flags)
+
+    @property
+    def dtype(self):
+        import torch
+        return torch.float32 if self.flags & PKM_F_FP32 else torch.bfloat16
+
+    @property
+    def runs(self) -> int:
+        """Scales per row of an 8-bit checkpoint of g or u."""
+        return -(-self.d_ff // CKPT8_RUN)
+
+
+def pkm_ffn_saved_bytes(dims: FfnDims, field: str) -> int:
+    return int(load().pkm_ffn_saved_bytes(ctypes.byref(dims.c()), FFN_SAVED_FIELDS.index(field)))
+
+
+def pkm_ffn_workspace_bytes(dims: FfnDims, which: int) -> int:
+    return int(load().pkm_ffn_workspace_bytes(ctypes.byref(dims.c()), which))
+
+
+def alloc_ffn_saved(dims: FfnDims, device="cuda") -> dict:
+    """Caller-owned buffers pkm_ffn_forward writes and pkm_ffn_backward reads (torch)."""
+    import torch
+    if dims.flags & PKM_FFN_CKPT8:
+        g, gs = alloc_ckpt8(dims.N, dims.d_ff, device)
+        u, us = alloc_ckpt8(dims.N, dims.d_ff, device)
+        return dict(g=g, u=u, g_scale=gs, u_scale=us)
+    g, u = (torch.empty(dims.N, dims.d_ff, dtype=dims.dtype, device=device) for _ in range(2))
+    return dict(g=g, u=u, g_scale=None, u_scale=None)
+
+
+def alloc_ffn_workspace(dims: FfnDims, which: int, device="cuda"):
+    import torch
+    return torch.empty(max(pkm_ffn_workspace_bytes(dims, which), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def _ffn_saved_c(dims: FfnDims, saved: dict) -> pkm_ffn_saved:
+    if dims.flags & PKM_FFN_CKPT8:
+        import torch
+        codes, runs = (dims.N, dims.runs * CKPT8_RUN), (dims.N, dims.runs)
+        return pkm_ffn_saved(*(_tensor(saved.get(k), f"saved[{k!r}]", torch.int8, codes)
+                               for k in ("g", "u")),
+                             *(_tensor(saved.get(k), f"saved[{k!r}]", torch.float32, runs)
+                               for k in ("g_scale", "u_scale")))
+    return pkm_ffn_saved(*(_tensor(saved.get(k), f"saved[{k!r}]", dims.dtype, (dims.N, dims.d_ff))
+                           for k in ("g", "u")), None, None)
+
+
+def _ffn_weights(d: FfnDims, Wg, Wu, Wd) -> tuple:
+    return (_tensor(Wg, "Wg", d.dtype, (d.d_ff, d.d_in)),
+            _tensor(Wu, "Wu", d.dtype, (d.d_ff, d.d_in)),
+            _tensor(Wd, "Wd", d.dtype, (d.d_out, d.d_ff)))
+
+
+def pkm_ffn_forward(dims: FfnDims, x, Wg, Wu, Wd, y, saved: dict | None = None, workspace=None,
+                    workspace_bytes: int = 0, stream=None) -> None:
+    """y = (act(x Wg^T) * (x Wu^T)) Wd^T; ``saved`` (alloc_ffn_saved) keeps what
+    pkm_ffn_backward needs, None keeps nothing."""
+    d = dims
+    s = None if saved is None else ctypes.byref(_ffn_saved_c(d, saved))
+    ws, ws_bytes = _ffn_workspace(workspace, workspace_bytes)
+    _check(load().pkm_ffn_forward(
+        ctypes.byref(d.c()), _tensor(x, "x", d.dtype, (d.N, d.d_in)), *_ffn_weights(d, Wg, Wu, Wd),
+        _tensor(y, "y", d.dtype, (d.N, d.d_out)), s, ws, ws_bytes, _stream(stream)),
+        "pkm_ffn_forward")
+
+
+def pkm_ffn_backward(dims: FfnDims, x, Wg, Wu, Wd, saved: dict, dy, dx=None, dWg=None, dWu=None,
+                     dWd=None, workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    """Gradients of sum(dy * y).  dx is overwritten; dWg, dWu, dWd are fp32 and accumulate, or
+    with PKM_FFN_GRAD_BF16 bf16 and overwritten.  A gradient that is None is skipped."""
+    import torch
+    d = dims
+    ws, ws_bytes = _ffn_workspace(workspace, workspace_bytes)
+    wt = torch.bfloat16 if d.flags & PKM_FFN_GRAD_BF16 else torch.float32
+    _check(load().pkm_ffn_backward(
+        ctypes.byref(d.c()), _tensor(x, "x", d.dtype, (d.N, d.d_in)), *_ffn_weights(d, Wg, Wu, Wd),
+        ctypes.byref(_ffn_saved_c(d, saved)), _tensor(dy, "dy", d.dtype, (d.N, d.d_out)),
+        _tensor(dx, "dx", d.dtype, (d.N, d.d_in), True),
+        _tensor(dWg, "dWg", wt, (d.d_ff, d.d_in), True),
+        _tensor(dWu, "dWu", wt, (d.d_ff, d.d_in), True),
+        _tensor(dWd, "dWd", wt, (d.d_out, d.d_ff), True), ws, ws_bytes, _stream(stream)),
+        "pkm_ffn_backward")
+
+
+# ------------------------------------------------------- 8-bit activation checkpoints
+def alloc_ckpt8(rows: int, cols: int, device="cuda") -> tuple:
+    """(codes, scale) of an 8-bit checkpoint of a [rows, cols] activation."""
+    import torch
+    runs = -(-cols // CKPT8_RUN)
+    return (torch.empty(rows, runs * CKPT8_RUN, dtype=torch.int8, device=device),
+            torch.empty(rows, runs, dtype=torch.float32, device=device))
+
+
+def _ckpt8(values, name, codes, scale):
+    import torch
+    if values.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name}: bfloat16 or float32 wanted, got {values.dtype}")
+    if values.dim() != 2:
+        raise ValueError(f"{name}: two dimensions wanted, got {values.dim()}")
+    rows, cols = values.shape
+    runs = -(-cols // CKPT8_RUN)
+    return (rows, cols, PKM_F_FP32 if values.dtype == torch.float32 else 0,
+            _tensor(values, name, values.dtype, (rows, cols)),
+            _tensor(codes, "codes", torch.int8, (rows, runs * CKPT8_RUN)),
+            _tensor(scale, "scale", torch.float32, (rows, runs)))
+
+
+def pkm_ckpt8_pack(src, codes, scale, stream=None) -> None:
+    """``src`` [rows, cols] bf16 or fp32 into 8-bit codes and a scale per 32 columns."""
+    rows, cols, flags, v, c, s = _ckpt8(src, "src", codes, scale)
+    _check(load().pkm_ckpt8_pack(rows, cols, flags, v, c, s, _stream(stream)), "pkm_ckpt8_pack")
+
+
+def pkm_ckpt8_unpack(codes, scale, dst, stream=None) -> None:
+    """The values (codes * scale) into ``dst`` [rows, cols], bf16 or fp32."""
+    rows, cols, flags, v, c, s = _ckpt8(dst, "dst", codes, scale)
+    _check(load().pkm_ckpt8_unpack(rows, cols, flags, c, s, v, _stream(stream)),
+           "pkm_ckpt8_unpack")
+
+
+# ------------------------------------------------------- products with 4-bit weights
+# A 4-bit matrix is the pair (codes, scale): codes uint8 [d_out, d_in / 2], scale bf16
+# [d_out, ceil(d_in / group)].
+
+def alloc_w4(d_out: int, d_in: int, group: int, device="cuda") -> tuple:
+    import torch
+    return (torch.empty(d_out, d_in // 2, dtype=torch.uint8, device=device),
+            torch.empty(d_out, -(-d_in // group), dtype=torch.bfloat16, device=device))
+
+
+def _w4(W, name: str, d_out: int, d_in: int, group: int) -> pkm_w4:
+    import torch
+    if group <= 0:
+        raise ValueError(f"group: a positive multiple of 32 wanted, got {group}")
+    codes, scale = W
+    return pkm_w4(_tensor(codes, f"{name} codes", torch.uint8, (d_out, d_in // 2)),
+                  _tensor(scale, f"{name} scale", torch.bfloat16, (d_out, -(-d_in // group))))
+
+
+def _w4_matrix(t, name: str):
+    import torch
+    if t.dim() != 2:
+        raise ValueError(f"{name}: two dimensions wanted, got {t.dim()}")
+    return _tensor(t, name, torch.bfloat16, tuple(t.shape))
+
+
+def pkm_w4_pack(W, codes, scale, group: int = 64, stream=None) -> None:
+    """A bf16 matrix ``W`` [d_out, d_in] into 4-bit codes and a bf16 scale per group."""
+    w = _w4_matrix(W, "W")
+    q = _w4((codes, scale), "packed", *W.shape, group)
+    _check(load().pkm_w4_pack(*W.shape, group, w, q.codes, q.scale, _stream(stream)),
+           "pkm_w4_pack")
+
+
+def pkm_w4_unpack(codes, scale, W, group: int = 64, stream=None) -> None:
+    """The bf16 matrix the codes stand for."""
+    w = _w4_matrix(W, "W")
+    q = _w4((codes, scale), "packed", *W.shape, group)
+    _check(load().pkm_w4_unpack(*W.shape, group, ctypes.byref(q), w, _stream(stream)),
+           "pkm_w4_unpack")
+
+
+def pkm_w4_matvec(x, codes, scale, y, group: int = 64, stream=None) -> None:
+    """y [N, d_out] fp32 = x W^T for up to PKM_W4_MAX_TOKENS rows of bf16 ``x``."""
+    import torch
+    xp = _w4_matrix(x, "x")
+    N, d_in = x.shape
+    d_out = codes.shape[0]
+    q = _w4((codes, scale), "W", d_out, d_in, group)
+    _check(load().pkm_w4_matvec(N, d_in, d_out, group, xp, ctypes.byref(q),
+                                _tensor(y, "y", torch.float32, (N, d_out)), _stream(stream)),
+           "pkm_w4_matvec")
+
+
+def pkm_w4_ffn(dims: FfnDims, x, Wg, Wu, Wd, y, group: int = 64, workspace=None,
+               workspace_bytes: int = 0, stream=None) -> None:
+    """pkm_ffn_forward with 4-bit weights, each a (codes, scale) pair, for up to
+    PKM_W4_MAX_TOKENS tokens."""
+    d = dims
+    ws, ws_bytes = _ffn_workspace(workspace, workspace_bytes)
+    g, u, o = (_w4(Wg, "Wg", d.d_ff, d.d_in, group), _w4(Wu, "Wu", d.d_ff, d.d_in, group),
+               _w4(Wd, "Wd", d.d_out, d.d_ff, group))
+    _check(load().pkm_w4_ffn(ctypes.byref(d.c()), group, _tensor(x, "x", d.dtype, (d.N, d.d_in)),
+                             ctypes.byref(g), ctypes.byref(u), ctypes.byref(o),
+                             _tensor(y, "y", d.dtype, (d.N, d.d_out)), ws, ws_bytes,
+                             _stream(stream)), "pkm_w4_ffn")

@@ -1,0 +1,186 @@
+"""Host-side behaviour of the gated feed-forward block, the 8-bit checkpoints and the 4-bit
+products (no GPU): sizes, refusals before any device work, and the reference's own gradients
+against differences."""
+import ctypes
+
+import pytest
+import torch
+
+from product_key_memory_pkm_b200 import build as B
+from product_key_memory_pkm_b200 import pkm as P
+
+from . import ffn_ref as R
+
+FAKE = 1 << 20  # aligned, never dereferenced: every call below is refused before a launch
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    B.build()
+    return P.load()
+
+
+def _d(**kw):
+    base = dict(N=64, d_in=64, d_ff=136, d_out=72)
+    base.update(kw)
+    return P.FfnDims(**base)
+
+
+def test_struct_sizes():
+    assert ctypes.sizeof(P.pkm_ffn_dims) == 32
+    assert ctypes.sizeof(P.pkm_ffn_saved) == 4 * ctypes.sizeof(ctypes.c_void_p)
+    assert ctypes.sizeof(P.pkm_w4) == 2 * ctypes.sizeof(ctypes.c_void_p)
+
+
+def test_saved_and_workspace_sizes():
+    d = _d()
+    assert P.pkm_ffn_saved_bytes(d, "g") == 64 * 136 * 2
+    assert P.pkm_ffn_saved_bytes(_d(flags=P.PKM_F_FP32), "u") == 64 * 136 * 4
+    assert P.pkm_ffn_saved_bytes(d, "g_scale") == 0
+    c8 = _d(flags=P.PKM_FFN_CKPT8)
+    assert P.pkm_ffn_saved_bytes(c8, "g") == 64 * 160       # 136 columns in runs of 32
+    assert P.pkm_ffn_saved_bytes(c8, "u_scale") == 64 * 5 * 4
+    saved = P.alloc_ffn_saved(c8, device="cpu")
+    for f in P.FFN_SAVED_FIELDS:
+        assert saved[f].numel() * saved[f].element_size() == P.pkm_ffn_saved_bytes(c8, f)
+    for which in (P.PKM_FWD, P.PKM_BWD):
+        assert P.pkm_ffn_workspace_bytes(d, which) > 0
+        assert P.pkm_ffn_workspace_bytes(_d(N=0), which) == 0
+        assert P.pkm_ffn_workspace_bytes(_d(act=7), which) == 0
+    assert P.pkm_ffn_workspace_bytes(d, P.PKM_FWD_FUSED) == 0
+
+
+BAD_DIMS = [dict(N=-1), dict(d_in=0), dict(d_ff=-8), dict(d_out=0), dict(d_in=60), dict(d_ff=132),
+            dict(d_out=71), dict(act=2), dict(act=-1), dict(flags=0x400), dict(flags=P.PKM_F_IDW),
+            dict(flags=P.PKM_F_FP32 | P.PKM_FFN_GRAD_BF16)]
+
+
+def _fwd(d, x=FAKE, y=FAKE, Wg=FAKE, Wd=FAKE, saved=None, ws=FAKE, wsb=1 << 30):
+    s = None if saved is None else ctypes.byref(P.pkm_ffn_saved(*saved))
+    return P.load().pkm_ffn_forward(ctypes.byref(d.c()), x, Wg, FAKE, Wd, y, s, ws, wsb, None)
+
+
+def _bwd(d, saved=(FAKE, FAKE, None, None), dy=FAKE, dx=FAKE, dWg=FAKE, ws=FAKE, wsb=1 << 30):
+    s = None if saved is None else ctypes.byref(P.pkm_ffn_saved(*saved))
+    return P.load().pkm_ffn_backward(ctypes.byref(d.c()), FAKE, FAKE, FAKE, FAKE, s, dy, dx, dWg,
+                                     None, None, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw", BAD_DIMS)
+def test_bad_dims_are_refused(kw):
+    assert _fwd(_d(**kw)) == P.PKM_ERR_INVALID_ARG
+    assert _bwd(_d(**kw)) == P.PKM_ERR_INVALID_ARG
+    assert P.pkm_ffn_saved_bytes(_d(**kw), "g") == 0
+
+
+def test_block_refusals():
+    d, c8 = _d(), _d(flags=P.PKM_FFN_CKPT8)
+    bad = P.PKM_ERR_INVALID_ARG
+    for kw in (dict(x=None), dict(x=FAKE + 2), dict(y=None), dict(Wg=FAKE + 8), dict(Wd=None),
+               dict(saved=(None, FAKE, None, None)), dict(saved=(FAKE, FAKE + 4, None, None))):
+        assert _fwd(d, **kw) == bad
+    assert _fwd(c8, saved=(FAKE, FAKE, FAKE, None)) == bad   # 8-bit codes need both scales
+    for kw in (dict(saved=None), dict(dy=None), dict(dx=FAKE + 4), dict(dWg=FAKE + 4)):
+        assert _bwd(d, **kw) == bad
+    assert _bwd(c8) == bad
+    need = P.pkm_ffn_workspace_bytes(d, P.PKM_FWD)
+    assert _fwd(d, ws=None) == P.PKM_ERR_WORKSPACE
+    assert _fwd(d, wsb=need - 1) == P.PKM_ERR_WORKSPACE
+    assert _fwd(d, ws=FAKE + 128) == P.PKM_ERR_WORKSPACE
+    assert _bwd(d, wsb=P.pkm_ffn_workspace_bytes(d, P.PKM_BWD) - 1) == P.PKM_ERR_WORKSPACE
+    assert _fwd(_d(d_ff=(1 << 20) + 8)) == P.PKM_ERR_UNSUPPORTED
+    assert _fwd(_d(N=(1 << 30) + 1)) == P.PKM_ERR_UNSUPPORTED
+    assert _fwd(_d(N=0), x=None, y=None, ws=None, wsb=0) == P.PKM_OK
+    assert _bwd(_d(N=0), saved=None, dy=None, ws=None, wsb=0) == P.PKM_OK
+    assert P.load().pkm_ffn_forward(None, *[FAKE] * 5, None, FAKE, 1 << 30, None) == bad
+
+
+def test_checkpoint_refusals():
+    L = P.load()
+    for fn in (L.pkm_ckpt8_pack, L.pkm_ckpt8_unpack):
+        assert fn(-1, 64, 0, FAKE, FAKE, FAKE, None) == P.PKM_ERR_INVALID_ARG
+        assert fn(4, 0, 0, FAKE, FAKE, FAKE, None) == P.PKM_ERR_INVALID_ARG
+        assert fn(4, 60, 0, FAKE, FAKE, FAKE, None) == P.PKM_ERR_INVALID_ARG
+        assert fn(4, 64, P.PKM_F_SIMT, FAKE, FAKE, FAKE, None) == P.PKM_ERR_INVALID_ARG
+        for i in range(3):
+            for bad in (None, FAKE + 4):
+                p = [FAKE] * 3
+                p[i] = bad
+                assert fn(4, 64, 0, *p, None) == P.PKM_ERR_INVALID_ARG
+        assert fn(0, 64, 0, None, None, None, None) == P.PKM_OK
+
+
+def test_w4_refusals():
+    L = P.load()
+    W = P.pkm_w4(FAKE, FAKE)
+
+    def mv(N=4, d_in=64, d_out=72, group=64, x=FAKE, w=W, y=FAKE):
+        return L.pkm_w4_matvec(N, d_in, d_out, group, x, None if w is None else ctypes.byref(w),
+                               y, None)
+
+    bad = P.PKM_ERR_INVALID_ARG
+    for kw in (dict(N=-1), dict(d_in=48), dict(d_in=0), dict(d_out=0), dict(group=0),
+               dict(group=-32), dict(group=48), dict(x=None), dict(y=FAKE + 4), dict(w=None),
+               dict(w=P.pkm_w4(FAKE + 8, FAKE)), dict(w=P.pkm_w4(FAKE, None))):
+        assert mv(**kw) == bad, kw
+    assert mv(N=P.PKM_W4_MAX_TOKENS + 1) == P.PKM_ERR_UNSUPPORTED
+    assert mv(d_out=(1 << 20) + 1) == P.PKM_ERR_UNSUPPORTED
+    assert mv(N=0, x=None, y=None) == P.PKM_OK
+    assert L.pkm_w4_pack(8, 48, 32, FAKE, FAKE, FAKE, None) == bad
+    assert L.pkm_w4_pack(8, 64, 32, None, FAKE, FAKE, None) == bad
+    assert L.pkm_w4_unpack(8, 64, 32, ctypes.byref(W), None, None) == bad
+
+    def ffn(d, group=64, ws=FAKE, wsb=1 << 30, wd=W):
+        return L.pkm_w4_ffn(ctypes.byref(d.c()), group, FAKE, ctypes.byref(W), ctypes.byref(W),
+                            ctypes.byref(wd), FAKE, ws, wsb, None)
+
+    d = _d(N=8, d_ff=96)
+    assert ffn(_d(N=8, d_ff=136)) == bad             # d_ff not a multiple of 32
+    assert ffn(_d(N=8, d_ff=96, flags=P.PKM_F_FP32)) == bad
+    assert ffn(_d(N=65, d_ff=96)) == P.PKM_ERR_UNSUPPORTED
+    assert ffn(d, group=16) == bad
+    assert ffn(d, wd=P.pkm_w4(None, FAKE)) == bad
+    assert ffn(d, wsb=16) == P.PKM_ERR_WORKSPACE
+    assert ffn(_d(N=0, d_ff=96), ws=None, wsb=0) == P.PKM_OK
+
+
+def test_binding_checks_its_tensors():
+    """Wrong type, shape, order or place is refused before the library is called."""
+    d = _d(N=2)
+    t = dict(x=torch.zeros(2, 64), Wg=torch.zeros(136, 64), Wu=torch.zeros(136, 64),
+             Wd=torch.zeros(72, 136), y=torch.zeros(2, 72))
+    with pytest.raises(TypeError):
+        P.pkm_ffn_forward(d, **t)                                  # fp32 for bf16
+    t = {k: v.bfloat16() for k, v in t.items()}
+    with pytest.raises(ValueError, match="not on a GPU"):
+        P.pkm_ffn_forward(d, **t)
+    with pytest.raises(ValueError, match="shape"):
+        P.pkm_ffn_forward(d, **{**t, "x": t["x"][:1]})
+    with pytest.raises(ValueError, match="missing"):
+        P.pkm_ffn_forward(d, **{**t, "x": None})
+    with pytest.raises(ValueError, match="contiguous"):
+        P.pkm_ffn_forward(d, **{**t, "x": torch.zeros(64, 2).bfloat16().t()})
+    with pytest.raises(TypeError):
+        P.pkm_ckpt8_pack(torch.zeros(2, 64, dtype=torch.float16), *P.alloc_ckpt8(2, 64, "cpu"))
+    with pytest.raises(ValueError):
+        P.pkm_w4_matvec(t["x"], *P.alloc_w4(72, 64, 64, "cpu"), torch.zeros(2, 72))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_reference_gradients_against_differences(act):
+    """The formulas every kernel is held to are the derivatives of the forward's formula."""
+    gen = torch.Generator().manual_seed(3)
+    n, di, f, do = 5, 8, 16, 8
+    mk = lambda *s: torch.randn(*s, generator=gen, dtype=torch.float64)  # noqa: E731
+    t = dict(x=mk(n, di), Wg=mk(f, di), Wu=mk(f, di), Wd=mk(do, f))
+    dy = mk(n, do)
+    fw = R.forward(act, **t, r=0.0)
+    gr = R.backward(act, *t.values(), fw["g"][0], fw["u"][0], dy, 0.0)
+    eps = 1e-5
+    for name, grad in (("x", "dx"), ("Wg", "dWg"), ("Wu", "dWu"), ("Wd", "dWd")):
+        v = mk(*t[name].shape)
+        side = [(R.forward(act, **{**t, name: t[name] + s * eps * v}, r=0.0)["y"][0] * dy).sum()
+                for s in (1, -1)]
+        diff = (side[0] - side[1]) / (2 * eps)
+        # the difference's own error: eps^2 times the third derivative (order 1e3 here at most)
+        assert abs((diff - (gr[grad][0] * v).sum()).item()) <= 1e-7 * (1 + abs(diff.item()))
