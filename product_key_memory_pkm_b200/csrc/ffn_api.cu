@@ -79,7 +79,7 @@ pkm_status make_plan(const pkm_ffn_dims* d, FfnPlan* p) {
 }
 
 size_t workspace_bytes_of(const FfnPlan& p, bool backward) {
-  return ffn_simt_workspace(p, backward);
+  return p.simt ? ffn_simt_workspace(p, backward) : ffn_tc_workspace(p, backward);
 }
 
 pkm_status check_workspace(size_t need, const void* ws, size_t bytes) {
@@ -156,7 +156,9 @@ pkm_status pkm_ffn_forward(const pkm_ffn_dims* d, const void* x, const void* Wg,
   FfnPlan p;
   PKM_TRY(make_plan(d, &p));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return cuda_status(launch_ffn_fwd_simt(p, x, Wg, Wu, Wd, y, saved, workspace, st));
+  return cuda_status(p.simt
+                         ? launch_ffn_fwd_simt(p, x, Wg, Wu, Wd, y, saved, workspace, st)
+                         : launch_ffn_fwd_tc(p, x, Wg, Wu, Wd, y, saved, workspace, st));
 }
 
 pkm_status pkm_ffn_backward(const pkm_ffn_dims* d, const void* x, const void* Wg, const void* Wu,
@@ -172,8 +174,8 @@ pkm_status pkm_ffn_backward(const pkm_ffn_dims* d, const void* x, const void* Wg
   FfnPlan p;
   PKM_TRY(make_plan(d, &p));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return cuda_status(
-      launch_ffn_bwd_simt(p, x, Wg, Wu, Wd, *saved, dy, dx, dWg, dWu, dWd, workspace, st));
+  const auto run = p.simt ? launch_ffn_bwd_simt : launch_ffn_bwd_tc;
+  return cuda_status(run(p, x, Wg, Wu, Wd, *saved, dy, dx, dWg, dWu, dWd, workspace, st));
 }
 
 pkm_status pkm_ckpt8_pack(int64_t rows, int32_t cols, uint32_t flags, const void* src,

@@ -99,6 +99,15 @@ cudaError_t launch_ffn_bwd_simt(const FfnPlan& p, const void* x, const void* Wg,
                                 const void* Wd, const pkm_ffn_saved& s, const void* dy, void* dx,
                                 void* dWg, void* dWu, void* dWd, void* ws, cudaStream_t st);
 
+// Tensor-core path (bf16 storage).
+size_t ffn_tc_workspace(const FfnPlan& p, bool backward);
+cudaError_t launch_ffn_fwd_tc(const FfnPlan& p, const void* x, const void* Wg, const void* Wu,
+                              const void* Wd, void* y, const pkm_ffn_saved* s, void* ws,
+                              cudaStream_t st);
+cudaError_t launch_ffn_bwd_tc(const FfnPlan& p, const void* x, const void* Wg, const void* Wu,
+                              const void* Wd, const pkm_ffn_saved& s, const void* dy, void* dx,
+                              void* dWg, void* dWu, void* dWd, void* ws, cudaStream_t st);
+
 cudaError_t launch_ckpt8_pack(int64_t rows, int cols, bool fp32, const void* src, int8_t* codes,
                               float* scale, int sm_count, cudaStream_t st);
 cudaError_t launch_ckpt8_unpack(int64_t rows, int cols, bool fp32, const int8_t* codes,
