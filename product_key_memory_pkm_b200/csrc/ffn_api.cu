@@ -101,7 +101,9 @@ pkm_status check_saved(const FfnPlan& p, const pkm_ffn_saved* s) {
 
 pkm_status validate_ckpt8(int64_t rows, int32_t cols, uint32_t flags) {
   if (rows < 0 || cols <= 0 || cols % 8 || (flags & ~PKM_F_FP32)) return PKM_ERR_INVALID_ARG;
-  if (cols > kMaxWidth || rows > ((int64_t)1 << 40)) return PKM_ERR_UNSUPPORTED;
+  if (rows > ((int64_t)1 << 38)) return PKM_ERR_UNSUPPORTED;
+  // grids of up to 2^31 - 1 blocks of 8192 values
+  if (cols > kMaxWidth || rows * ckpt_runs(cols) > ((int64_t)1 << 38)) return PKM_ERR_UNSUPPORTED;
   return PKM_OK;
 }
 
@@ -156,6 +158,8 @@ pkm_status pkm_ffn_forward(const pkm_ffn_dims* d, const void* x, const void* Wg,
   FfnPlan p;
   PKM_TRY(make_plan(d, &p));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!p.simt && !saved && p.N <= kFfnFewTokens)
+    return cuda_status(launch_ffn_few(p, x, Wg, Wu, Wd, y, workspace, st));
   return cuda_status(p.simt
                          ? launch_ffn_fwd_simt(p, x, Wg, Wu, Wd, y, saved, workspace, st)
                          : launch_ffn_fwd_tc(p, x, Wg, Wu, Wd, y, saved, workspace, st));
@@ -186,7 +190,7 @@ pkm_status pkm_ckpt8_pack(int64_t rows, int32_t cols, uint32_t flags, const void
   DeviceInfo info;
   if (!current_device(&info)) return PKM_ERR_CUDA;
   return cuda_status(launch_ckpt8_pack(rows, cols, flags & PKM_F_FP32, src, codes, scale,
-                                       info.sm_count, static_cast<cudaStream_t>(stream)));
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 pkm_status pkm_ckpt8_unpack(int64_t rows, int32_t cols, uint32_t flags, const int8_t* codes,
@@ -197,7 +201,7 @@ pkm_status pkm_ckpt8_unpack(int64_t rows, int32_t cols, uint32_t flags, const in
   DeviceInfo info;
   if (!current_device(&info)) return PKM_ERR_CUDA;
   return cuda_status(launch_ckpt8_unpack(rows, cols, flags & PKM_F_FP32, codes, scale, dst,
-                                         info.sm_count, static_cast<cudaStream_t>(stream)));
+                                         static_cast<cudaStream_t>(stream)));
 }
 
 pkm_status pkm_w4_pack(int32_t d_out, int32_t d_in, int32_t group, const void* W, uint8_t* codes,

@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t mag_bits(float a) { return __float_as_uint(a
 constexpr uint32_t kInfBits = 0x7f800000u;
 
 // The scale of a run whose largest magnitude has the bits `top`, and the factor that takes
-// its values to codes (0 for an all-zero or non-finite run).
+// its values to codes.  top: that magnitude, or -1 for a run with a non-finite value.
 struct CkptScale {
   float scale, inv, top;
 };
@@ -53,23 +53,57 @@ __device__ __forceinline__ CkptScale ckpt_scale(uint32_t top_bits) {
   if (top_bits >= kInfBits) {
     s.scale = __uint_as_float(0x7fc00000u);
     s.inv = 0.f;
-    s.top = 0.f;
+    s.top = -1.f;
   } else {
     s.scale = s.top / 127.f;
     s.inv = s.top > 0.f ? 127.f / s.top : 0.f;  // overflows to inf below 2^-121: see ckpt_code
   }
   return s;
 }
-// 127 a / top rounded to the nearest integer, halves to even.  The fp32 product is off by at
-// most 127 * 2^-23 = 1.5e-5, so only within 2e-5 of a half can it round the other way: there
-// the quotient is formed in 64 bits (127 a is exact, and a quotient that is not a half is
-// farther than 2^-26 from one).
-__device__ __forceinline__ int ckpt_code(float a, const CkptScale& s) {
-  if (s.top == 0.f) return 0;
-  const float q = a * s.inv;
-  const float r = rintf(q);
-  if (fabsf(fabsf(q - r) - 0.5f) > 2e-5f && s.top > 1e-30f) return (int)r;
-  return (int)rint((double)a * 127.0 / (double)s.top);
+// Code of one value, formed in 64 bits: 127 a is exact there, and a quotient that is not a
+// half is farther than 2^-26 from one, so its rounding decides nothing.
+__device__ __forceinline__ int ckpt_code_exact(float a, const CkptScale& s) {
+  return s.top <= 0.f ? 0 : (int)rint((double)a * 127.0 / (double)s.top);
+}
+// Codes of N values, four to a word: 127 a / top rounded to the nearest integer, halves to
+// even.  One fused multiply-add onto 1.5 * 2^23 leaves the rounded product in the low bits;
+// inv is off by 2^-24 of itself, the product by at most 127 * 2^-24 = 7.6e-6, so the rounding
+// can only be wrong where the product lies within that of a half.  There (1e-5 of a half, or a
+// run so small that inv overflows) the codes are formed in 64 bits instead: about one warp in
+// a hundred for N = 8.
+template <int N>
+__device__ __forceinline__ void ckpt_codes(const float (&a)[N], const CkptScale& s,
+                                           uint32_t (&w)[N / 4]) {
+  constexpr float kMagic = 12582912.f;
+  float far = 0.f;
+#pragma unroll
+  for (int j = 0; j < N / 4; ++j) {
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = a[4 * j + i], t = fmaf(v, s.inv, kMagic);
+      far = fmaxf(far, fabsf(fmaf(v, s.inv, kMagic - t)));
+      b[i] = __float_as_uint(t);
+    }
+    w[j] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  }
+  if (far > 0.5f - 1e-5f || (s.top < 1e-30f && s.top != 0.f)) {
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) {
+      w[j] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[j] |= ((uint32_t)ckpt_code_exact(a[4 * j + i], s) & 0xffu) << (8 * i);
+    }
+  }
+}
+// The four codes of a word as floats (exact): byte c ^ 0x80 as the low mantissa byte of 2^23
+// stands for 2^23 + 128 + c.
+__device__ __forceinline__ void ckpt_floats4(uint32_t w, float (&v)[4]) {
+  const uint32_t x = w ^ 0x80808080u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7440 | i)) - 8388736.f;
 }
 
 // ---------------------------------------------------------------- plan
@@ -109,9 +143,9 @@ cudaError_t launch_ffn_bwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
                               void* dWg, void* dWu, void* dWd, void* ws, cudaStream_t st);
 
 cudaError_t launch_ckpt8_pack(int64_t rows, int cols, bool fp32, const void* src, int8_t* codes,
-                              float* scale, int sm_count, cudaStream_t st);
+                              float* scale, cudaStream_t st);
 cudaError_t launch_ckpt8_unpack(int64_t rows, int cols, bool fp32, const int8_t* codes,
-                                const float* scale, void* dst, int sm_count, cudaStream_t st);
+                                const float* scale, void* dst, cudaStream_t st);
 
 cudaError_t launch_w4_pack(int d_out, int d_in, int group, const void* W, uint8_t* codes,
                            void* scale, cudaStream_t st);
@@ -121,5 +155,9 @@ cudaError_t launch_w4_matvec(int64_t N, int d_in, int d_out, int group, const vo
                              const W4Mat& W, float* y, int sm_count, cudaStream_t st);
 cudaError_t launch_w4_ffn(const FfnPlan& p, int group, const void* x, const W4Mat& Wg,
                           const W4Mat& Wu, const W4Mat& Wd, void* y, void* ws, cudaStream_t st);
+// The forward of a few tokens with nothing kept (bf16 weights).  ws: h [N][d_ff] bf16.
+constexpr int64_t kFfnFewTokens = 16;
+cudaError_t launch_ffn_few(const FfnPlan& p, const void* x, const void* Wg, const void* Wu,
+                           const void* Wd, void* y, void* ws, cudaStream_t st);
 
 }  // namespace pkm

@@ -132,15 +132,11 @@ struct GateProb {
 #pragma unroll
     for (int j = 0; j < 32; ++j) top = max(top, r[j] & 0x7fffffffu);
     const CkptScale s = ckpt_scale(top);
+    float a[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(r[j]);
     uint32_t w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t v = 0;
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        v |= ((uint32_t)ckpt_code(__uint_as_float(r[4 * j + b]), s) & 0xffu) << (8 * b);
-      w[j] = v;
-    }
+    ckpt_codes(a, s, w);
     uint4* d = reinterpret_cast<uint4*>(codes + run_idx * kCkptRun);
     d[0] = make_uint4(w[0], w[1], w[2], w[3]);
     d[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -249,14 +245,20 @@ struct GateGradProb {
   __device__ static void prefetch(const Params& P, const Tile& t, const PairEpi& e, Early& k) {
     fetch(P, (int64_t)t.m0 + e.row0 + e.lane, t.n0 + e.set * 32, k);
   }
-  // Columns 2j and 2j + 1 of the piece.
-  __device__ static float2 pair_of(const uint4* q, float scale, int j) {
+  // Columns 4j .. 4j + 3 of the piece.
+  __device__ static void four_of(const uint4* q, float scale, int j, float (&v)[4]) {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(q);
     if (CKPT8) {
-      const uint32_t c = w[j >> 1] >> ((j & 1) * 16);
-      return make_float2((float)(int8_t)(c & 0xff) * scale, (float)(int8_t)((c >> 8) & 0xff) * scale);
+      ckpt_floats4(w[j], v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] *= scale;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        v[2 * i] = __uint_as_float(w[2 * j + i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[2 * j + i] & 0xffff0000u);
+      }
     }
-    return make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
   }
   __device__ static void epilogue(const Params& P, const Tile& t, const PairEpi& e, Early& k) {
     const int y0 = t.m0 + e.row0;
@@ -271,15 +273,25 @@ struct GateGradProb {
       if ((piece + 2) * 32 < t.w) fetch(P, row, c0 + 64, k);
       tmem_wait_ld(d);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float2 g = pair_of(now.g, now.sg, j), u = pair_of(now.u, now.su, j);
-        const float d0 = __uint_as_float(d[2 * j]), d1 = __uint_as_float(d[2 * j + 1]);
-        float a0, a1, s0, s1;
-        act_and_slope_fast<ACT>(g.x, &a0, &s0);
-        act_and_slope_fast<ACT>(g.y, &a1, &s1);
-        ph[j] = pack_bf16(a0 * u.x, a1 * u.y);
-        pg[j] = pack_bf16(d0 * u.x * s0, d1 * u.y * s1);
-        pu[j] = pack_bf16(d0 * a0, d1 * a1);
+      for (int j = 0; j < 8; ++j) {
+        float g[4], u[4], hh[4], dg[4], du[4];
+        four_of(now.g, now.sg, j, g);
+        four_of(now.u, now.su, j, u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float dh = __uint_as_float(d[4 * j + i]);
+          float a, slope;
+          act_and_slope_fast<ACT>(g[i], &a, &slope);
+          hh[i] = a * u[i];
+          dg[i] = dh * u[i] * slope;
+          du[i] = dh * a;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          ph[2 * j + i] = pack_bf16(hh[2 * i], hh[2 * i + 1]);
+          pg[2 * j + i] = pack_bf16(dg[2 * i], dg[2 * i + 1]);
+          pu[2 * j + i] = pack_bf16(du[2 * i], du[2 * i + 1]);
+        }
       }
       staging_free(e.lane);
       stage_bf16(e.stg, e.lane, ph);
