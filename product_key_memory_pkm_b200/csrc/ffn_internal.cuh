@@ -62,16 +62,22 @@ __device__ __forceinline__ CkptScale ckpt_scale(uint32_t top_bits) {
 }
 // Code of one value, formed in 64 bits: 127 a is exact there, and a quotient that is not a
 // half is farther than 2^-26 from one, so its rounding decides nothing.
-__device__ __forceinline__ int ckpt_code_exact(float a, const CkptScale& s) {
-  return s.top <= 0.f ? 0 : (int)rint((double)a * 127.0 / (double)s.top);
+__device__ __noinline__ inline int ckpt_code_exact(float a, float top) {
+  return top <= 0.f ? 0 : (int)rint((double)a * 127.0 / (double)top);
 }
 // Codes of N values, four to a word: 127 a / top rounded to the nearest integer, halves to
-// even.  One fused multiply-add onto 1.5 * 2^23 leaves the rounded product in the low bits;
-// inv is off by 2^-24 of itself, the product by at most 127 * 2^-24 = 7.6e-6, so the rounding
-// can only be wrong where the product lies within that of a half.  There (1e-5 of a half, or a
-// run so small that inv overflows) the codes are formed in 64 bits instead: about one warp in
-// a hundred for N = 8.
-template <int N>
+// even.  Adding 1.5 * 2^23 leaves the rounded number in the low bits.  The product a * inv is
+// off by up to 2^-23 of itself, so a quotient that is exactly a half needs care:
+//   BF16 (values exact in bf16): a quotient 127 a / top that is not a half is at least 2^-16
+//     of it away (254 A 2^z against M (2r + 1) with 8-bit integers A and M), so rounding the
+//     product to 20 significant bits first turns the halves into exact halves and moves no
+//     other across one.  Such halves are frequent there, and this has no branch.
+//   else: where a product lies within 1e-5 of a half, the exact remainder decides.  With
+//     127 a = hi + lo (both fp32) and r the candidate, e = hi - r top is exact (a multiple of
+//     top's last place, below top), so is 2|e| - top, and the sum with 2 lo has the sign of
+//     the exact remainder less a half.
+// A run whose largest magnitude is below 1e-30 (inv may overflow) is formed in 64 bits.
+template <bool BF16, int N>
 __device__ __forceinline__ void ckpt_codes(const float (&a)[N], const CkptScale& s,
                                            uint32_t (&w)[N / 4]) {
   constexpr float kMagic = 12582912.f;
@@ -81,19 +87,41 @@ __device__ __forceinline__ void ckpt_codes(const float (&a)[N], const CkptScale&
     uint32_t b[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float v = a[4 * j + i], t = fmaf(v, s.inv, kMagic);
-      far = fmaxf(far, fabsf(fmaf(v, s.inv, kMagic - t)));
-      b[i] = __float_as_uint(t);
+      const float v = a[4 * j + i];
+      if (BF16) {
+        const float q = v * s.inv, c = q * 17.f;
+        b[i] = __float_as_uint(__fadd_rn(__fsub_rn(c, __fsub_rn(c, q)), kMagic));
+      } else {
+        const float t = fmaf(v, s.inv, kMagic);
+        far = fmaxf(far, fabsf(fmaf(v, s.inv, kMagic - t)));
+        b[i] = __float_as_uint(t);
+      }
     }
     w[j] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   }
-  if (far > 0.5f - 1e-5f || (s.top < 1e-30f && s.top != 0.f)) {
+  if (!BF16 && far > 0.5f - 1e-5f) {
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) {
+      w[j] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = a[4 * j + i];
+        float r = __fsub_rn(fmaf(v, s.inv, kMagic), kMagic);
+        const float hi = __fmul_rn(v, 127.f), lo = fmaf(v, 127.f, -hi);
+        const float e = fmaf(-r, s.top, hi), up = e < 0.f ? -1.f : 1.f;
+        const float over = __fadd_rn(fmaf(2.f, fabsf(e), -s.top), 2.f * lo * up);
+        if (over > 0.f || (over == 0.f && ((int)r & 1))) r += up;
+        w[j] |= ((uint32_t)(int)r & 0xffu) << (8 * i);
+      }
+    }
+  }
+  if (s.top < 1e-30f && s.top != 0.f) {
 #pragma unroll
     for (int j = 0; j < N / 4; ++j) {
       w[j] = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        w[j] |= ((uint32_t)ckpt_code_exact(a[4 * j + i], s) & 0xffu) << (8 * i);
+        w[j] |= ((uint32_t)ckpt_code_exact(a[4 * j + i], s.top) & 0xffu) << (8 * i);
     }
   }
 }

@@ -6,6 +6,7 @@
 // and a thread has kUnroll such chunks in flight.  The arithmetic is about 7 instructions per
 // value (ckpt_codes), half of what the memory time leaves room for.
 #include <algorithm>
+#include <type_traits>
 
 #include "ffn_internal.cuh"
 
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(kTpb) pack_kernel(int64_t chunks, int per_row,
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const CkptScale s = ckpt_scale(top);
     uint32_t w[2];
-    ckpt_codes(v, s, w);
+    ckpt_codes<std::is_same<T, bf>::value>(v, s, w);
     if (c < chunks) {
       *reinterpret_cast<uint2*>(codes + c * 8) = make_uint2(w[0], w[1]);
       if ((threadIdx.x & 3) == 0) scale[c >> 2] = s.scale;

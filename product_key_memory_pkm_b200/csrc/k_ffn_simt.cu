@@ -18,7 +18,7 @@ __device__ __forceinline__ void put(bf* p, float v) { *p = __float2bfloat16_rn(v
 __device__ __forceinline__ void keep8(float v, int64_t run_idx, int lane, int8_t* codes,
                                       float* scale) {
   const CkptScale s = ckpt_scale(__reduce_max_sync(0xffffffffu, mag_bits(v)));
-  codes[run_idx * kCkptRun + lane] = (int8_t)ckpt_code_exact(v, s);
+  codes[run_idx * kCkptRun + lane] = (int8_t)ckpt_code_exact(v, s.top);
   if (lane == 0) scale[run_idx] = s.scale;
 }
 

@@ -136,7 +136,7 @@ struct GateProb {
 #pragma unroll
     for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(r[j]);
     uint32_t w[8];
-    ckpt_codes(a, s, w);
+    ckpt_codes<false>(a, s, w);
     uint4* d = reinterpret_cast<uint4*>(codes + run_idx * kCkptRun);
     d[0] = make_uint4(w[0], w[1], w[2], w[3]);
     d[1] = make_uint4(w[4], w[5], w[6], w[7]);

@@ -510,39 +510,54 @@ def pkm_shard_scatter_dw(dims: Dims, perm, dw_ret, dw, stream=None) -> None:
 # Unlike the raw-address calls above, these check the tensors they are given: type, shape,
 # contiguity and device (integer addresses pass unchecked).
 
-def _tensor(t, name: str, dtype, shape: tuple, optional: bool = False) -> int | None:
-    """Address of a contiguous ``shape`` tensor of ``dtype`` on the current device."""
-    if t is None:
-        if optional:
-            return None
-        raise ValueError(f"{name} is missing")
-    if isinstance(t, int):
-        return t
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: {dtype} wanted, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {shape} wanted, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
-    _on_current(t, name)
-    return t.data_ptr()
+class _Checked:
+    """Checks of one call's tensors and the call's stream.  Few-token calls run for a few
+    microseconds on the GPU, so this avoids what costs one on the host: repeated imports and
+    the wrapper objects of torch.cuda.current_stream()."""
+    __slots__ = ("torch", "device")
 
+    def __init__(self):
+        import torch
+        self.torch = torch
+        self.device = None  # the current device, once a GPU tensor has been seen
 
-def _on_current(t, name: str) -> None:
-    import torch
-    if not t.is_cuda:
-        raise ValueError(f"{name} is not on a GPU")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"{torch.cuda.current_device()}")
+    def __call__(self, t, name: str, dtype, shape: tuple, optional: bool = False) -> int | None:
+        """Address of a contiguous ``shape`` tensor of ``dtype`` on the current device."""
+        if t is None:
+            if optional:
+                return None
+            raise ValueError(f"{name} is missing")
+        if isinstance(t, int):
+            return t
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: {dtype} wanted, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {shape} wanted, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} is not contiguous")
+        self.place(t, name)
+        return t.data_ptr()
 
+    def place(self, t, name: str) -> None:
+        if not t.is_cuda:
+            raise ValueError(f"{name} is not on a GPU")
+        if self.device is None:
+            self.device = self.torch._C._cuda_getDevice()
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} is on {t.device}, the current device is {self.device}")
 
-def _ffn_workspace(workspace, workspace_bytes):
-    if workspace is not None and not isinstance(workspace, int):
+    def stream(self, stream):
+        if stream is None and self.device is not None:
+            return self.torch._C._cuda_getCurrentRawStream(self.device)
+        return _stream(stream)
+
+    def workspace(self, workspace, workspace_bytes):
+        if workspace is None or isinstance(workspace, int):
+            return workspace, workspace_bytes
         if not workspace.is_contiguous():
             raise ValueError("workspace is not contiguous")
-        _on_current(workspace, "workspace")
-    return _ptr(workspace), _ws(workspace, workspace_bytes)
+        self.place(workspace, "workspace")
+        return workspace.data_ptr(), workspace_bytes or workspace.nbytes
 
 
 @dataclass(frozen=True)
@@ -555,8 +570,13 @@ class FfnDims:
     act: int = PKM_ACT_SILU
     flags: int = 0
 
+    def __post_init__(self):
+        s = pkm_ffn_dims(self.N, self.d_in, self.d_ff, self.d_out, self.act, self.flags)
+        object.__setattr__(self, "_c", s)
+        object.__setattr__(self, "_ref", ctypes.byref(s))
+
     def c(self) -> pkm_ffn_dims:
-        return pkm_ffn_dims(self.N, self.d_in, self.d_ff, self.d_out, self.act, self.flags)
+        return self._c
 
     @property
     def dtype(self):
@@ -594,53 +614,50 @@ def alloc_ffn_workspace(dims: FfnDims, which: int, device="cuda"):
                        device=device)
 
 
-def _ffn_saved_c(dims: FfnDims, saved: dict) -> pkm_ffn_saved:
-    if dims.flags & PKM_FFN_CKPT8:
-        import torch
-        codes, runs = (dims.N, dims.runs * CKPT8_RUN), (dims.N, dims.runs)
-        return pkm_ffn_saved(*(_tensor(saved.get(k), f"saved[{k!r}]", torch.int8, codes)
-                               for k in ("g", "u")),
-                             *(_tensor(saved.get(k), f"saved[{k!r}]", torch.float32, runs)
-                               for k in ("g_scale", "u_scale")))
-    return pkm_ffn_saved(*(_tensor(saved.get(k), f"saved[{k!r}]", dims.dtype, (dims.N, dims.d_ff))
-                           for k in ("g", "u")), None, None)
-
-
-def _ffn_weights(d: FfnDims, Wg, Wu, Wd) -> tuple:
-    return (_tensor(Wg, "Wg", d.dtype, (d.d_ff, d.d_in)),
-            _tensor(Wu, "Wu", d.dtype, (d.d_ff, d.d_in)),
-            _tensor(Wd, "Wd", d.dtype, (d.d_out, d.d_ff)))
+def _ffn_saved_c(ck: _Checked, d: FfnDims, saved: dict) -> pkm_ffn_saved:
+    if d.flags & PKM_FFN_CKPT8:
+        i8, f32 = ck.torch.int8, ck.torch.float32
+        codes, runs = (d.N, d.runs * CKPT8_RUN), (d.N, d.runs)
+        return pkm_ffn_saved(ck(saved.get("g"), "saved g", i8, codes),
+                             ck(saved.get("u"), "saved u", i8, codes),
+                             ck(saved.get("g_scale"), "saved g_scale", f32, runs),
+                             ck(saved.get("u_scale"), "saved u_scale", f32, runs))
+    dt, shape = d.dtype, (d.N, d.d_ff)
+    return pkm_ffn_saved(ck(saved.get("g"), "saved g", dt, shape),
+                         ck(saved.get("u"), "saved u", dt, shape), None, None)
 
 
 def pkm_ffn_forward(dims: FfnDims, x, Wg, Wu, Wd, y, saved: dict | None = None, workspace=None,
                     workspace_bytes: int = 0, stream=None) -> None:
     """y = (act(x Wg^T) * (x Wu^T)) Wd^T; ``saved`` (alloc_ffn_saved) keeps what
     pkm_ffn_backward needs, None keeps nothing."""
-    d = dims
-    s = None if saved is None else ctypes.byref(_ffn_saved_c(d, saved))
-    ws, ws_bytes = _ffn_workspace(workspace, workspace_bytes)
-    _check(load().pkm_ffn_forward(
-        ctypes.byref(d.c()), _tensor(x, "x", d.dtype, (d.N, d.d_in)), *_ffn_weights(d, Wg, Wu, Wd),
-        _tensor(y, "y", d.dtype, (d.N, d.d_out)), s, ws, ws_bytes, _stream(stream)),
-        "pkm_ffn_forward")
+    d, ck = dims, _Checked()
+    dt = d.dtype
+    xp, yp = ck(x, "x", dt, (d.N, d.d_in)), ck(y, "y", dt, (d.N, d.d_out))
+    g, u = ck(Wg, "Wg", dt, (d.d_ff, d.d_in)), ck(Wu, "Wu", dt, (d.d_ff, d.d_in))
+    o = ck(Wd, "Wd", dt, (d.d_out, d.d_ff))
+    s = None if saved is None else ctypes.byref(_ffn_saved_c(ck, d, saved))
+    ws, ws_bytes = ck.workspace(workspace, workspace_bytes)
+    _check(load().pkm_ffn_forward(d._ref, xp, g, u, o, yp, s, ws, ws_bytes, ck.stream(stream)),
+           "pkm_ffn_forward")
 
 
 def pkm_ffn_backward(dims: FfnDims, x, Wg, Wu, Wd, saved: dict, dy, dx=None, dWg=None, dWu=None,
                      dWd=None, workspace=None, workspace_bytes: int = 0, stream=None) -> None:
     """Gradients of sum(dy * y).  dx is overwritten; dWg, dWu, dWd are fp32 and accumulate, or
     with PKM_FFN_GRAD_BF16 bf16 and overwritten.  A gradient that is None is skipped."""
-    import torch
-    d = dims
-    ws, ws_bytes = _ffn_workspace(workspace, workspace_bytes)
-    wt = torch.bfloat16 if d.flags & PKM_FFN_GRAD_BF16 else torch.float32
-    _check(load().pkm_ffn_backward(
-        ctypes.byref(d.c()), _tensor(x, "x", d.dtype, (d.N, d.d_in)), *_ffn_weights(d, Wg, Wu, Wd),
-        ctypes.byref(_ffn_saved_c(d, saved)), _tensor(dy, "dy", d.dtype, (d.N, d.d_out)),
-        _tensor(dx, "dx", d.dtype, (d.N, d.d_in), True),
-        _tensor(dWg, "dWg", wt, (d.d_ff, d.d_in), True),
-        _tensor(dWu, "dWu", wt, (d.d_ff, d.d_in), True),
-        _tensor(dWd, "dWd", wt, (d.d_out, d.d_ff), True), ws, ws_bytes, _stream(stream)),
-        "pkm_ffn_backward")
+    d, ck = dims, _Checked()
+    dt = d.dtype
+    wt = ck.torch.bfloat16 if d.flags & PKM_FFN_GRAD_BF16 else ck.torch.float32
+    xs, ins, outs = (d.N, d.d_in), (d.d_ff, d.d_in), (d.d_out, d.d_ff)
+    args = (ck(x, "x", dt, xs), ck(Wg, "Wg", dt, ins), ck(Wu, "Wu", dt, ins),
+            ck(Wd, "Wd", dt, outs), ctypes.byref(_ffn_saved_c(ck, d, saved)),
+            ck(dy, "dy", dt, (d.N, d.d_out)), ck(dx, "dx", dt, xs, True),
+            ck(dWg, "dWg", wt, ins, True), ck(dWu, "dWu", wt, ins, True),
+            ck(dWd, "dWd", wt, outs, True))
+    ws, ws_bytes = ck.workspace(workspace, workspace_bytes)
+    _check(load().pkm_ffn_backward(d._ref, *args, ws, ws_bytes, ck.stream(stream)),
+           "pkm_ffn_backward")
 
 
 # ------------------------------------------------------- 8-bit activation checkpoints
@@ -652,30 +669,31 @@ def alloc_ckpt8(rows: int, cols: int, device="cuda") -> tuple:
             torch.empty(rows, runs, dtype=torch.float32, device=device))
 
 
-def _ckpt8(values, name, codes, scale):
-    import torch
-    if values.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{name}: bfloat16 or float32 wanted, got {values.dtype}")
+def _ckpt8(ck: _Checked, values, name, codes, scale):
+    dt, f32 = values.dtype, ck.torch.float32
+    if dt != f32 and dt != ck.torch.bfloat16:
+        raise TypeError(f"{name}: bfloat16 or float32 wanted, got {dt}")
     if values.dim() != 2:
         raise ValueError(f"{name}: two dimensions wanted, got {values.dim()}")
     rows, cols = values.shape
     runs = -(-cols // CKPT8_RUN)
-    return (rows, cols, PKM_F_FP32 if values.dtype == torch.float32 else 0,
-            _tensor(values, name, values.dtype, (rows, cols)),
-            _tensor(codes, "codes", torch.int8, (rows, runs * CKPT8_RUN)),
-            _tensor(scale, "scale", torch.float32, (rows, runs)))
+    return (rows, cols, PKM_F_FP32 if dt == f32 else 0, ck(values, name, dt, (rows, cols)),
+            ck(codes, "codes", ck.torch.int8, (rows, runs * CKPT8_RUN)),
+            ck(scale, "scale", f32, (rows, runs)))
 
 
 def pkm_ckpt8_pack(src, codes, scale, stream=None) -> None:
     """``src`` [rows, cols] bf16 or fp32 into 8-bit codes and a scale per 32 columns."""
-    rows, cols, flags, v, c, s = _ckpt8(src, "src", codes, scale)
-    _check(load().pkm_ckpt8_pack(rows, cols, flags, v, c, s, _stream(stream)), "pkm_ckpt8_pack")
+    ck = _Checked()
+    rows, cols, flags, v, c, s = _ckpt8(ck, src, "src", codes, scale)
+    _check(load().pkm_ckpt8_pack(rows, cols, flags, v, c, s, ck.stream(stream)), "pkm_ckpt8_pack")
 
 
 def pkm_ckpt8_unpack(codes, scale, dst, stream=None) -> None:
     """The values (codes * scale) into ``dst`` [rows, cols], bf16 or fp32."""
-    rows, cols, flags, v, c, s = _ckpt8(dst, "dst", codes, scale)
-    _check(load().pkm_ckpt8_unpack(rows, cols, flags, c, s, v, _stream(stream)),
+    ck = _Checked()
+    rows, cols, flags, v, c, s = _ckpt8(ck, dst, "dst", codes, scale)
+    _check(load().pkm_ckpt8_unpack(rows, cols, flags, c, s, v, ck.stream(stream)),
            "pkm_ckpt8_unpack")
 
 
@@ -689,59 +707,60 @@ def alloc_w4(d_out: int, d_in: int, group: int, device="cuda") -> tuple:
             torch.empty(d_out, -(-d_in // group), dtype=torch.bfloat16, device=device))
 
 
-def _w4(W, name: str, d_out: int, d_in: int, group: int) -> pkm_w4:
-    import torch
+def _w4(ck: _Checked, W, name: str, d_out: int, d_in: int, group: int) -> pkm_w4:
     if group <= 0:
         raise ValueError(f"group: a positive multiple of 32 wanted, got {group}")
     codes, scale = W
-    return pkm_w4(_tensor(codes, f"{name} codes", torch.uint8, (d_out, d_in // 2)),
-                  _tensor(scale, f"{name} scale", torch.bfloat16, (d_out, -(-d_in // group))))
+    return pkm_w4(ck(codes, f"{name} codes", ck.torch.uint8, (d_out, d_in // 2)),
+                  ck(scale, f"{name} scale", ck.torch.bfloat16, (d_out, -(-d_in // group))))
 
 
-def _w4_matrix(t, name: str):
-    import torch
+def _matrix(ck: _Checked, t, name: str):
     if t.dim() != 2:
         raise ValueError(f"{name}: two dimensions wanted, got {t.dim()}")
-    return _tensor(t, name, torch.bfloat16, tuple(t.shape))
+    return ck(t, name, ck.torch.bfloat16, t.shape)
 
 
 def pkm_w4_pack(W, codes, scale, group: int = 64, stream=None) -> None:
     """A bf16 matrix ``W`` [d_out, d_in] into 4-bit codes and a bf16 scale per group."""
-    w = _w4_matrix(W, "W")
-    q = _w4((codes, scale), "packed", *W.shape, group)
-    _check(load().pkm_w4_pack(*W.shape, group, w, q.codes, q.scale, _stream(stream)),
+    ck = _Checked()
+    w = _matrix(ck, W, "W")
+    q = _w4(ck, (codes, scale), "packed", *W.shape, group)
+    _check(load().pkm_w4_pack(*W.shape, group, w, q.codes, q.scale, ck.stream(stream)),
            "pkm_w4_pack")
 
 
 def pkm_w4_unpack(codes, scale, W, group: int = 64, stream=None) -> None:
     """The bf16 matrix the codes stand for."""
-    w = _w4_matrix(W, "W")
-    q = _w4((codes, scale), "packed", *W.shape, group)
-    _check(load().pkm_w4_unpack(*W.shape, group, ctypes.byref(q), w, _stream(stream)),
+    ck = _Checked()
+    w = _matrix(ck, W, "W")
+    q = _w4(ck, (codes, scale), "packed", *W.shape, group)
+    _check(load().pkm_w4_unpack(*W.shape, group, ctypes.byref(q), w, ck.stream(stream)),
            "pkm_w4_unpack")
 
 
 def pkm_w4_matvec(x, codes, scale, y, group: int = 64, stream=None) -> None:
     """y [N, d_out] fp32 = x W^T for up to PKM_W4_MAX_TOKENS rows of bf16 ``x``."""
-    import torch
-    xp = _w4_matrix(x, "x")
+    ck = _Checked()
+    xp = _matrix(ck, x, "x")
     N, d_in = x.shape
     d_out = codes.shape[0]
-    q = _w4((codes, scale), "W", d_out, d_in, group)
-    _check(load().pkm_w4_matvec(N, d_in, d_out, group, xp, ctypes.byref(q),
-                                _tensor(y, "y", torch.float32, (N, d_out)), _stream(stream)),
-           "pkm_w4_matvec")
+    q = _w4(ck, (codes, scale), "W", d_out, d_in, group)
+    yp = ck(y, "y", ck.torch.float32, (N, d_out))
+    _check(load().pkm_w4_matvec(N, d_in, d_out, group, xp, ctypes.byref(q), yp,
+                                ck.stream(stream)), "pkm_w4_matvec")
 
 
 def pkm_w4_ffn(dims: FfnDims, x, Wg, Wu, Wd, y, group: int = 64, workspace=None,
                workspace_bytes: int = 0, stream=None) -> None:
     """pkm_ffn_forward with 4-bit weights, each a (codes, scale) pair, for up to
     PKM_W4_MAX_TOKENS tokens."""
-    d = dims
-    ws, ws_bytes = _ffn_workspace(workspace, workspace_bytes)
-    g, u, o = (_w4(Wg, "Wg", d.d_ff, d.d_in, group), _w4(Wu, "Wu", d.d_ff, d.d_in, group),
-               _w4(Wd, "Wd", d.d_out, d.d_ff, group))
-    _check(load().pkm_w4_ffn(ctypes.byref(d.c()), group, _tensor(x, "x", d.dtype, (d.N, d.d_in)),
-                             ctypes.byref(g), ctypes.byref(u), ctypes.byref(o),
-                             _tensor(y, "y", d.dtype, (d.N, d.d_out)), ws, ws_bytes,
-                             _stream(stream)), "pkm_w4_ffn")
+    d, ck = dims, _Checked()
+    b16 = ck.torch.bfloat16
+    xp, yp = ck(x, "x", b16, (d.N, d.d_in)), ck(y, "y", b16, (d.N, d.d_out))
+    g = _w4(ck, Wg, "Wg", d.d_ff, d.d_in, group)
+    u = _w4(ck, Wu, "Wu", d.d_ff, d.d_in, group)
+    o = _w4(ck, Wd, "Wd", d.d_out, d.d_ff, group)
+    ws, ws_bytes = ck.workspace(workspace, workspace_bytes)
+    _check(load().pkm_w4_ffn(d._ref, group, xp, ctypes.byref(g), ctypes.byref(u), ctypes.byref(o),
+                             yp, ws, ws_bytes, ck.stream(stream)), "pkm_w4_ffn")
