@@ -19,6 +19,7 @@
 // are too few to fill the SMs, 2 or 4 CTAs of a cluster split k further and add up through
 // distributed shared memory.  Every sum has a fixed order.
 #include <algorithm>
+#include <atomic>
 
 #include "ffn_internal.cuh"
 
@@ -46,6 +47,21 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t w, int j) {
   const __nv_bfloat162 off = __floats2bfloat162_rn(136.f, 136.f);
   const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m), off);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The products of a unit start from zero.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1,
+                                               uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// 8 columns of a token in the order a word's codes come out in: (0,4) (1,5) (2,6) (3,7).
+__device__ __forceinline__ uint4 w4_order(const uint4& q) {
+  return make_uint4(__byte_perm(q.x, q.z, 0x5410), __byte_perm(q.x, q.z, 0x7632),
+                    __byte_perm(q.y, q.w, 0x5410), __byte_perm(q.y, q.w, 0x7632));
 }
 
 // 8 columns of a token, zeros for no token or no column.
@@ -102,23 +118,33 @@ struct W4Unit {
       }
     }
   }
-  // acc += this unit's products with 8 tokens, whose columns of word j are xv[j]
-  __device__ void mac(float (&acc)[4], const uint4 (&xv)[2]) const {
-    float t[4] = {0.f, 0.f, 0.f, 0.f};
+  __device__ static uint4 order(const uint4& q) { return w4_order(q); }
+  // The codes of the lane's rows as A operands: a[j][2 i + r] = pair i of row r's word j.
+  struct A {
+    uint32_t a[2][8];
+  };
+  __device__ A operands() const {
+    A o;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o.a[j][i] = w4_pair(w[i & 1][j], i >> 1);
+    return o;
+  }
+  // acc += this unit's products with 8 tokens, whose ordered columns of word j are xv[j]
+  __device__ void mac(float (&acc)[4], const A& o, const uint4 (&xv)[2]) const {
+    float t[4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      mma16816(t, w4_pair(w[0][j], 0), w4_pair(w[1][j], 0), w4_pair(w[0][j], 1),
-               w4_pair(w[1][j], 1), __byte_perm(xv[j].x, xv[j].z, 0x5410),
-               __byte_perm(xv[j].x, xv[j].z, 0x7632));
-      mma16816(t, w4_pair(w[0][j], 2), w4_pair(w[1][j], 2), w4_pair(w[0][j], 3),
-               w4_pair(w[1][j], 3), __byte_perm(xv[j].y, xv[j].w, 0x5410),
-               __byte_perm(xv[j].y, xv[j].w, 0x7632));
+      const uint32_t(&a)[8] = o.a[j];
+      if (HALF || j == 0)
+        mma16816_first(t, a[0], a[1], a[2], a[3], xv[j].x, xv[j].y);
+      else
+        mma16816(t, a[0], a[1], a[2], a[3], xv[j].x, xv[j].y);
+      mma16816(t, a[4], a[5], a[6], a[7], xv[j].z, xv[j].w);
       if (HALF || j == 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc[i] = fmaf(to_f32(s[i >> 1][HALF ? j : 0]), t[i], acc[i]);
-          t[i] = 0.f;
-        }
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(to_f32(s[i >> 1][HALF ? j : 0]), t[i], acc[i]);
       }
     }
   }
@@ -148,7 +174,10 @@ struct W16Unit {
                              : make_uint4(0, 0, 0, 0);
       }
   }
-  __device__ void mac(float (&acc)[4], const uint4 (&xv)[2]) const {
+  __device__ static uint4 order(const uint4& q) { return q; }
+  struct A {};
+  __device__ A operands() const { return A{}; }
+  __device__ void mac(float (&acc)[4], const A&, const uint4 (&xv)[2]) const {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       mma16816(acc, w[0][j].x, w[1][j].x, w[0][j].y, w[1][j].y, xv[j].x, xv[j].y);
@@ -221,12 +250,15 @@ __global__ void __launch_bounds__(kTpb) few_kernel(int N, int d_in, int d_out, i
     for (int b = 0; b < kBatch; ++b) {
       if (u + b >= u1) break;
       const int k0 = (u + b) * Unit::kCols;
+      typename Unit::A a[M];
+#pragma unroll
+      for (int m = 0; m < M; ++m) a[m] = w[m][b].operands();
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const uint4 xv[2] = {x8(x, N, d_in, t * 8 + g, Unit::col(k0, c, 0)),
-                             x8(x, N, d_in, t * 8 + g, Unit::col(k0, c, 1))};
+        const uint4 xv[2] = {Unit::order(x8(x, N, d_in, t * 8 + g, Unit::col(k0, c, 0))),
+                             Unit::order(x8(x, N, d_in, t * 8 + g, Unit::col(k0, c, 1)))};
 #pragma unroll
-        for (int m = 0; m < M; ++m) w[m][b].mac(acc[m][t], xv);
+        for (int m = 0; m < M; ++m) w[m][b].mac(acc[m][t], a[m], xv);
       }
     }
     if (u + kBatch < u1) fetch(u + kBatch);
@@ -289,6 +321,133 @@ __global__ void __launch_bounds__(kTpb) few_kernel(int N, int d_in, int d_out, i
   }
 }
 
+// ------------------------------------------------------------------ many rows
+// More than 16 tokens and many output rows: what bounds few_kernel there is not the weights but
+// every 16 rows reading all of x again.  Here a CTA per SM keeps x (or a chunk of its columns)
+// in shared memory, in operand order, and each of its warps takes 32 rows through all of k, so
+// a read of x serves 32 rows.  The number of warps is chosen so that the rows fill whole
+// rounds of the SMs.  Bound by issuing mma.sync with their operands.
+constexpr int kWideRows = 32, kWideWarps = 12, kWideBatch = 2;
+constexpr int kWideSmem = 225 * 1024;
+
+template <bool HALF, int NT>
+__global__ void __launch_bounds__(32 * kWideWarps, 1)
+    wide_kernel(int N, int d_in, int d_out, int group, int chunk, const bf* __restrict__ x, W4Mat W,
+                float* __restrict__ y) {
+  using Unit = W4Unit<HALF>;
+  constexpr int T = NT * 8;
+  extern __shared__ __align__(16) unsigned char xs[];
+  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  // rows of x are apart by an odd number of 16-byte columns (HALF: of 64-byte ones), so the 8
+  // lanes that read 16 bytes at a time meet no bank twice
+  const int pitch = chunk * 2 + (HALF ? 64 : 16);
+  const int tiles = (d_out + kWideRows - 1) / kWideRows;
+  const int chunks = (d_in + chunk - 1) / chunk;
+  for (int first = 0; first < tiles; first += gridDim.x * warps) {  // a round, same for all CTAs
+    const int tile = first + warp * gridDim.x + blockIdx.x;
+    const bool mine = tile < tiles;
+    const typename Unit::Src s0(W, d_out, d_in, group, tile * kWideRows, g);
+    const typename Unit::Src s1(W, d_out, d_in, group, tile * kWideRows + 16, g);
+    float acc[2][NT][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[r][t][i] = 0.f;
+    for (int ch = 0; ch < chunks; ++ch) {
+      const int k0 = ch * chunk, cols = min(chunk, d_in - k0);
+      const int u0 = k0 / 64, u1 = u0 + (cols + 63) / 64;
+      Unit cur[2][kWideBatch], nxt[2][kWideBatch];
+      const auto fetch = [&](Unit (&w)[2][kWideBatch], int u) {
+#pragma unroll
+        for (int b = 0; b < kWideBatch; ++b)
+          if (u + b < u1) {
+            w[0][b].load(s0, u + b, c);
+            w[1][b].load(s1, u + b, c);
+          }
+      };
+      if (mine) fetch(cur, u0);
+      if (first == 0 || chunks > 1) {
+        if (ch > 0 || first > 0) __syncthreads();  // the chunk before has been read
+        const int blocks = (cols + 63) / 64 * 8;   // 8-column blocks, whole units
+        for (int e = threadIdx.x; e < T * blocks; e += blockDim.x) {
+          const int n = e / blocks, b = e % blocks;
+          *reinterpret_cast<uint4*>(xs + n * pitch + b * 16) =
+              w4_order(x8(x, N, d_in, n, k0 + b * 8));
+        }
+        __syncthreads();
+      }
+      if (!mine) continue;
+      for (int u = u0; u < u1; u += kWideBatch) {
+        if (u + kWideBatch < u1) fetch(nxt, u + kWideBatch);
+#pragma unroll
+        for (int b = 0; b < kWideBatch; ++b) {
+          if (u + b >= u1) break;
+          const typename Unit::A a0 = cur[0][b].operands(), a1 = cur[1][b].operands();
+          const unsigned char* xb = xs + g * pitch;
+          const int o0 = Unit::col((u + b - u0) * 64, c, 0) * 2;
+          const int o1 = Unit::col((u + b - u0) * 64, c, 1) * 2;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const uint4 xv[2] = {*reinterpret_cast<const uint4*>(xb + t * 8 * pitch + o0),
+                                 *reinterpret_cast<const uint4*>(xb + t * 8 * pitch + o1)};
+            cur[0][b].mac(acc[0][t], a0, xv);
+            cur[1][b].mac(acc[1][t], a1, xv);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < kWideBatch; ++b) {
+          cur[0][b] = nxt[0][b];
+          cur[1][b] = nxt[1][b];
+        }
+      }
+    }
+    if (!mine) continue;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = t * 8 + 2 * c + (i & 1), o = tile * kWideRows + r * 16 + g + 8 * (i >> 1);
+          if (n < N && o < d_out) y[(int64_t)n * d_out + o] = acc[r][t][i];
+        }
+  }
+}
+
+template <bool HALF, int NT>
+cudaError_t launch_wide(int N, int d_in, int d_out, int group, const bf* x, const W4Mat& W,
+                        float* y, int sm_count, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    e = cudaFuncSetAttribute(wide_kernel<HALF, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kWideSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or((uint64_t)1 << dev, std::memory_order_release);
+  }
+  const int pad = HALF ? 64 : 16;
+  const int most = (kWideSmem / (NT * 8) - pad) / 2 / 64 * 64;
+  const int chunk = std::min((d_in + 63) / 64 * 64, most);
+  const int tiles = (d_out + kWideRows - 1) / kWideRows;
+  const int per_sm = (tiles + sm_count - 1) / sm_count;
+  const int rounds = (per_sm + kWideWarps - 1) / kWideWarps;
+  const int warps = (per_sm + rounds - 1) / rounds;
+  wide_kernel<HALF, NT><<<std::min(tiles, sm_count), 32 * warps, (size_t)NT * 8 * (chunk * 2 + pad), st>>>(
+      N, d_in, d_out, group, chunk, x, W, y);
+  PKM_COUNT(1);
+  return cudaGetLastError();
+}
+
+// Rows enough that every SM has several warps of 32.
+bool wide_form(int64_t N, int d_out, int sm_count) {
+  return N > 16 && d_out >= 4 * kWideRows * sm_count;
+}
+
 // CTAs of a cluster along k: more while the grid leaves SMs empty and every warp still has
 // two units.
 int split_of(int d_out, int d_in, int sm_count) {
@@ -348,8 +507,16 @@ cudaError_t w4(int N, int d_in, int d_out, int group, const bf* x, const W4Mat& 
 
 cudaError_t launch_w4_matvec(int64_t N, int d_in, int d_out, int group, const void* x,
                              const W4Mat& W, float* y, int sm_count, cudaStream_t st) {
-  return w4<Few::kF32, 0>((int)N, d_in, d_out, group, static_cast<const bf*>(x), W, W, y, true,
-                          sm_count, st);
+  const bf* xb = static_cast<const bf*>(x);
+  const int n = (int)N;
+  if (wide_form(N, d_out, sm_count)) {
+    if (group % 64)
+      return N <= 32 ? launch_wide<true, 4>(n, d_in, d_out, group, xb, W, y, sm_count, st)
+                     : launch_wide<true, 8>(n, d_in, d_out, group, xb, W, y, sm_count, st);
+    return N <= 32 ? launch_wide<false, 4>(n, d_in, d_out, group, xb, W, y, sm_count, st)
+                   : launch_wide<false, 8>(n, d_in, d_out, group, xb, W, y, sm_count, st);
+  }
+  return w4<Few::kF32, 0>(n, d_in, d_out, group, xb, W, W, y, true, sm_count, st);
 }
 
 cudaError_t launch_w4_ffn(const FfnPlan& p, int group, const void* x, const W4Mat& Wg,

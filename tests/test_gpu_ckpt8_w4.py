@@ -133,7 +133,11 @@ def random_w4(seed, o, i, group):
 @pytest.mark.parametrize("group", [32, 64, 96, 128, 512])
 @pytest.mark.parametrize("n,i,o", [(1, 32, 1), (1, 64, 9), (2, 96, 17), (1, 1600, 2048),
                                    (3, 1600, 100), (8, 2016, 333), (9, 1024, 64), (16, 640, 1000),
-                                   (17, 4128, 72), (33, 160, 50), (64, 1600, 515), (64, 32, 8)])
+                                   (17, 4128, 72), (33, 160, 50), (64, 1600, 515), (64, 32, 8),
+                                   # many rows: whole rounds of the SMs and ragged ones, x in
+                                   # one piece and in several
+                                   (17, 96, 19001), (32, 1600, 40000), (40, 2016, 18944),
+                                   (64, 32, 19999), (64, 4128, 19000), (16, 160, 20000)])
 def test_w4_matvec(n, i, o, group):
     x = rnd(n, n, i).bfloat16()
     codes, scale = random_w4(i, o, i, group)
