@@ -9,10 +9,10 @@
 // instruction), not for their rate; a CTA-wide tcgen05 tile would have to put the weights
 // through shared memory first.
 //
-//   4-bit   a lane's 8 codes are bytes of one row; (w >> 4j) & 0x000f000f is the pair of codes
-//           (j, j + 4), and 0x4300 | code is the bf16 number 128 + code, from which 136 is
-//           taken (exact).  Products of codes with bf16 x are exact, a unit of 64 columns is
-//           summed in fp32 and then scaled by its group's scale in fp32.
+//   4-bit   a word is 8 neighbouring codes of one row; spread over 16-bit halves, 0x4300 | code
+//           is the bf16 number 128 + code, from which 136 is taken (exact).  Products of codes
+//           with bf16 x are exact; the products of a word's 32 columns (four lanes) are summed
+//           in fp32 and then scaled by their group's scale in fp32.
 //   bf16    a lane's 16 bytes are 8 columns of one row.
 //
 // A CTA's 8 warps split k for 16 output rows and add up through shared memory; where the rows
@@ -32,38 +32,38 @@ constexpr int kWarps = 8, kTpb = 32 * kWarps;
 constexpr int kRows = 16;   // output rows of a CTA
 constexpr int kBatch = 4;   // units a warp has in flight
 
+// (Not volatile: the compiler may interleave independent products.)
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Codes (j, j + 4) of a word as bf16 numbers code - 8.
-__device__ __forceinline__ uint32_t w4_pair(uint32_t w, int j) {
-  const uint32_t m = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+// The codes of a word as pairs (0,1) (2,3) (4,5) (6,7) of bf16 numbers code - 8.
+__device__ __forceinline__ void w4_pairs(uint32_t w, uint32_t (&p)[4]) {
+  const uint32_t odd = w >> 4;
   const __nv_bfloat162 off = __floats2bfloat162_rn(136.f, 136.f);
-  const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m), off);
-  return *reinterpret_cast<const uint32_t*>(&v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t m = (__byte_perm(w, odd, i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12)) &
+                        0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m), off);
+    p[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
 }
 
-// The products of a unit start from zero.
+// The products of a word start from zero.
 __device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1,
                                                uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// 8 columns of a token in the order a word's codes come out in: (0,4) (1,5) (2,6) (3,7).
-__device__ __forceinline__ uint4 w4_order(const uint4& q) {
-  return make_uint4(__byte_perm(q.x, q.z, 0x5410), __byte_perm(q.x, q.z, 0x7632),
-                    __byte_perm(q.y, q.w, 0x5410), __byte_perm(q.y, q.w, 0x7632));
-}
-
 // 8 columns of a token, zeros for no token or no column.
 __device__ __forceinline__ uint4 x8(const bf* x, int64_t N, int d_in, int n, int k) {
   return n < N && k < d_in ? *reinterpret_cast<const uint4*>(x + (int64_t)n * d_in + k)
@@ -71,119 +71,139 @@ __device__ __forceinline__ uint4 x8(const bf* x, int64_t N, int d_in, int n, int
 }
 
 // ------------------------------------------------------------------ weights
-// Weights of one unit for this lane's two rows (g and g + 8).
+// Weights of one unit for this lane's two rows (g and g + 8 of a tile of 16).
 //
 // 4-bit: a unit is 64 columns.  HALF = false (groups of whole units): the lane holds columns
 // [k0 + 16 c, +16) and one scale serves the unit.  HALF = true (groups of 32, 96, ...): columns
 // [k0 + 8 c, +8) and [k0 + 32 + 8 c, +8), each half with its own scale.
+struct W4Shape {
+  int d_in, d_out, ng;
+  uint32_t magic;  // quotient by a group's length in units (HALF: half units): see group_of
+  static W4Shape of(int d_in, int d_out, int group) {
+    const uint32_t per = (uint32_t)(group % 64 ? group / 32 : group / 64);
+    return W4Shape{d_in, d_out, (d_in + group - 1) / group,
+                   per == 1 ? 0u : (uint32_t)(((uint64_t)1 << 32) / per + 1)};
+  }
+  // i / per for i < 2^15, per <= 2^15: the error of magic, below per, adds i * per / 2^32 < 1/4
+  __device__ int group_of(int i) const { return magic ? (int)__umulhi((uint32_t)i, magic) : i; }
+};
 template <bool HALF>
 struct W4Unit {
   static constexpr int kCols = 64;
+  static constexpr int kScales = HALF ? 2 : 1;
   uint32_t w[2][2];  // [row][word]
-  bf s[2][HALF ? 2 : 1];
+  bf s[2][kScales];
 
   struct Src {
-    const uint8_t* row[2];
-    const bf* scale[2];
-    int d_in, group, ng;
-    __device__ Src(const W4Mat& W, int d_out, int d_in_, int group_, int o0, int g)
-        : d_in(d_in_), group(group_), ng((d_in_ + group_ - 1) / group_) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int64_t o = min(o0 + g + 8 * r, d_out - 1);  // rows past the last are not stored
-        row[r] = W.codes + o * (d_in / 2);
-        scale[r] = W.scale + o * ng;
-      }
+    const uint8_t* codes;
+    const bf* scale;
+    int next_c, next_s;  // from row g to row g + 8, in bytes and in scales
+    __device__ Src(const W4Mat& W, const W4Shape& sh, int o0, int g) {
+      // rows past the last are read as the last and not stored
+      const int64_t o = min(o0 + g, sh.d_out - 1), p = min(o0 + g + 8, sh.d_out - 1);
+      codes = W.codes + o * (sh.d_in / 2);
+      scale = W.scale + o * sh.ng;
+      next_c = (int)(p - o) * (sh.d_in / 2);
+      next_s = (int)(p - o) * sh.ng;
     }
   };
-  __device__ static int col(int k0, int c, int j) { return HALF ? k0 + 32 * j + 8 * c : k0 + 16 * c + 8 * j; }
-  __device__ void load(const Src& S, int u, int c) {
+  __device__ static int col(int k0, int c, int j) {
+    return HALF ? k0 + 32 * j + 8 * c : k0 + 16 * c + 8 * j;
+  }
+  __device__ void load(const Src& S, const W4Shape& sh, int u, int c) {
     const int k0 = u * kCols;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+      const uint8_t* row = S.codes + (r ? S.next_c : 0);
+      const bf* sc = S.scale + (r ? S.next_s : 0);
       if (HALF) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int k = col(k0, c, j);
-          w[r][j] = k < S.d_in ? __ldg(reinterpret_cast<const uint32_t*>(S.row[r] + k / 2)) : 0u;
-          s[r][j] = k0 + 32 * j < S.d_in ? S.scale[r][(k0 + 32 * j) / S.group] : bf(0.f);
+          w[r][j] = k < sh.d_in ? __ldg(reinterpret_cast<const uint32_t*>(row + k / 2)) : 0u;
+          s[r][kScales * j / 2] = k0 + 32 * j < sh.d_in ? sc[sh.group_of(2 * u + j)] : bf(0.f);
         }
       } else {
         const int k = col(k0, c, 0);
-        const uint2 q = k < S.d_in ? __ldg(reinterpret_cast<const uint2*>(S.row[r] + k / 2))
-                                   : make_uint2(0u, 0u);
+        const uint2 q = k < sh.d_in ? __ldg(reinterpret_cast<const uint2*>(row + k / 2))
+                                    : make_uint2(0u, 0u);
         w[r][0] = q.x;
         w[r][1] = q.y;
-        s[r][0] = S.scale[r][k0 / S.group];
+        s[r][0] = sc[sh.group_of(u)];
       }
     }
   }
-  __device__ static uint4 order(const uint4& q) { return w4_order(q); }
-  // The codes of the lane's rows as A operands: a[j][2 i + r] = pair i of row r's word j.
+  // The A operands and scales of word j.
   struct A {
-    uint32_t a[2][8];
+    uint32_t g[4], h[4];
+    float sg, sh;
   };
-  __device__ A operands() const {
+  __device__ A operands(int j) const {
     A o;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o.a[j][i] = w4_pair(w[i & 1][j], i >> 1);
+    w4_pairs(w[0][j], o.g);
+    w4_pairs(w[1][j], o.h);
+    o.sg = to_f32(s[0][kScales * j / 2]);
+    o.sh = to_f32(s[1][kScales * j / 2]);
     return o;
   }
-  // acc += this unit's products with 8 tokens, whose ordered columns of word j are xv[j]
-  __device__ void mac(float (&acc)[4], const A& o, const uint4 (&xv)[2]) const {
+  // acc += the word's products with 8 tokens, x their columns
+  __device__ static void mac(float (&acc)[4], const A& o, const uint4& x) {
     float t[4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t(&a)[8] = o.a[j];
-      if (HALF || j == 0)
-        mma16816_first(t, a[0], a[1], a[2], a[3], xv[j].x, xv[j].y);
-      else
-        mma16816(t, a[0], a[1], a[2], a[3], xv[j].x, xv[j].y);
-      mma16816(t, a[4], a[5], a[6], a[7], xv[j].z, xv[j].w);
-      if (HALF || j == 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = fmaf(to_f32(s[i >> 1][HALF ? j : 0]), t[i], acc[i]);
-      }
-    }
+    mma16816_first(t, o.g[0], o.h[0], o.g[1], o.h[1], x.x, x.y);
+    mma16816(t, o.g[2], o.h[2], o.g[3], o.h[3], x.z, x.w);
+    acc[0] = fmaf(o.sg, t[0], acc[0]);
+    acc[1] = fmaf(o.sg, t[1], acc[1]);
+    acc[2] = fmaf(o.sh, t[2], acc[2]);
+    acc[3] = fmaf(o.sh, t[3], acc[3]);
   }
 };
 
 // bf16: a unit is 64 columns, as two halves of 8 columns per lane.
+struct W16Shape {
+  int d_in, d_out;
+  static W16Shape of(int d_in, int d_out, int) { return W16Shape{d_in, d_out}; }
+};
 struct W16Unit {
   static constexpr int kCols = 64;
   uint4 w[2][2];  // [row][half]
 
   struct Src {
-    const bf* row[2];
-    int d_in;
-    __device__ Src(const bf* W, int d_out, int d_in_, int, int o0, int g) : d_in(d_in_) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) row[r] = W + (int64_t)min(o0 + g + 8 * r, d_out - 1) * d_in;
+    const bf* row;
+    int64_t next;
+    __device__ Src(const bf* W, const W16Shape& sh, int o0, int g) {
+      const int64_t o = min(o0 + g, sh.d_out - 1), p = min(o0 + g + 8, sh.d_out - 1);
+      row = W + o * sh.d_in;
+      next = (p - o) * sh.d_in;
     }
   };
   __device__ static int col(int k0, int c, int j) { return k0 + 32 * j + 8 * c; }
-  __device__ void load(const Src& S, int u, int c) {
+  __device__ void load(const Src& S, const W16Shape& sh, int u, int c) {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int k = col(u * kCols, c, j);
-        w[r][j] = k < S.d_in ? __ldcs(reinterpret_cast<const uint4*>(S.row[r] + k))
-                             : make_uint4(0, 0, 0, 0);
+        w[r][j] = k < sh.d_in
+                      ? __ldcs(reinterpret_cast<const uint4*>(S.row + (r ? S.next : 0) + k))
+                      : make_uint4(0, 0, 0, 0);
       }
   }
-  __device__ static uint4 order(const uint4& q) { return q; }
-  struct A {};
-  __device__ A operands() const { return A{}; }
-  __device__ void mac(float (&acc)[4], const A&, const uint4 (&xv)[2]) const {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      mma16816(acc, w[0][j].x, w[1][j].x, w[0][j].y, w[1][j].y, xv[j].x, xv[j].y);
-      mma16816(acc, w[0][j].z, w[1][j].z, w[0][j].w, w[1][j].w, xv[j].z, xv[j].w);
-    }
+  struct A {
+    uint4 g, h;
+  };
+  __device__ A operands(int j) const { return A{w[0][j], w[1][j]}; }
+  __device__ static void mac(float (&acc)[4], const A& o, const uint4& x) {
+    mma16816(acc, o.g.x, o.h.x, o.g.y, o.h.y, x.x, x.y);
+    mma16816(acc, o.g.z, o.h.z, o.g.w, o.h.w, x.z, x.w);
   }
+};
+struct W4Of {
+  using Mat = W4Mat;
+  using Shape = W4Shape;
+};
+struct W16Of {
+  using Mat = const bf*;
+  using Shape = W16Shape;
 };
 
 // ------------------------------------------------------------------ kernel
@@ -205,10 +225,11 @@ __device__ __forceinline__ void cluster_sync() {
 enum class Few { kF32, kBf16, kGate };  // y fp32, y bf16, or h = act(first) * second in bf16
 
 // NT: tokens in blocks of 8.  GATE uses both matrices, the others the first.
-template <class Unit, class Mat, int NT, Few OUT, int ACT>
-__global__ void __launch_bounds__(kTpb) few_kernel(int N, int d_in, int d_out, int group, int ks,
+template <class Unit, class Mat, class Shape, int NT, Few OUT, int ACT>
+__global__ void __launch_bounds__(kTpb) few_kernel(int N, Shape sh, int ks,
                                                    const bf* __restrict__ x, Mat W0, Mat W1,
                                                    void* __restrict__ out, bool first) {
+  const int d_in = sh.d_in, d_out = sh.d_out;
   constexpr int M = OUT == Few::kGate ? 2 : 1;
   constexpr int T = NT * 8;
   // a slot per warp, or per two warps where 8 would pass the static limit of 48 KiB
@@ -221,7 +242,7 @@ __global__ void __launch_bounds__(kTpb) few_kernel(int N, int d_in, int d_out, i
   const int per = (units + kWarps * ks - 1) / (kWarps * ks);
   const int u0 = (rank * kWarps + warp) * per, u1 = min(units, u0 + per);
 
-  const typename Unit::Src s0(W0, d_out, d_in, group, o0, g), s1(M == 2 ? W1 : W0, d_out, d_in, group, o0, g);
+  const typename Unit::Src s0(W0, sh, o0, g), s1(M == 2 ? W1 : W0, sh, o0, g);
   float acc[M][NT][4];
 #pragma unroll
   for (int m = 0; m < M; ++m)
@@ -235,8 +256,8 @@ __global__ void __launch_bounds__(kTpb) few_kernel(int N, int d_in, int d_out, i
 #pragma unroll
     for (int b = 0; b < kBatch; ++b)
       if (u + b < u1) {
-        w[0][b].load(s0, u + b, c);
-        if (M == 2) w[M - 1][b].load(s1, u + b, c);
+        w[0][b].load(s0, sh, u + b, c);
+        if (M == 2) w[M - 1][b].load(s1, sh, u + b, c);
       }
   };
   // weights do not depend on the kernel before, x of the second product does
@@ -250,15 +271,17 @@ __global__ void __launch_bounds__(kTpb) few_kernel(int N, int d_in, int d_out, i
     for (int b = 0; b < kBatch; ++b) {
       if (u + b >= u1) break;
       const int k0 = (u + b) * Unit::kCols;
-      typename Unit::A a[M];
 #pragma unroll
-      for (int m = 0; m < M; ++m) a[m] = w[m][b].operands();
+      for (int j = 0; j < 2; ++j) {
+        typename Unit::A a[M];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint4 xv[2] = {Unit::order(x8(x, N, d_in, t * 8 + g, Unit::col(k0, c, 0))),
-                             Unit::order(x8(x, N, d_in, t * 8 + g, Unit::col(k0, c, 1)))};
+        for (int m = 0; m < M; ++m) a[m] = w[m][b].operands(j);
 #pragma unroll
-        for (int m = 0; m < M; ++m) w[m][b].mac(acc[m][t], a[m], xv);
+        for (int t = 0; t < NT; ++t) {
+          const uint4 xv = x8(x, N, d_in, t * 8 + g, Unit::col(k0, c, j));
+#pragma unroll
+          for (int m = 0; m < M; ++m) Unit::mac(acc[m][t], a[m], xv);
+        }
       }
     }
     if (u + kBatch < u1) fetch(u + kBatch);
@@ -327,28 +350,33 @@ __global__ void __launch_bounds__(kTpb) few_kernel(int N, int d_in, int d_out, i
 // in shared memory, in operand order, and each of its warps takes 32 rows through all of k, so
 // a read of x serves 32 rows.  The number of warps is chosen so that the rows fill whole
 // rounds of the SMs.  Bound by issuing mma.sync with their operands.
-constexpr int kWideRows = 32, kWideWarps = 12, kWideBatch = 2;
+constexpr int kWideRows = 32, kWideWarps = 12, kWideAhead = 1;
 constexpr int kWideSmem = 225 * 1024;
+
+// 16 bytes global -> shared without registers; zeros when !has.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool has) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(has ? 16 : 0)
+               : "memory");
+}
 
 template <bool HALF, int NT>
 __global__ void __launch_bounds__(32 * kWideWarps, 1)
-    wide_kernel(int N, int d_in, int d_out, int group, int chunk, const bf* __restrict__ x, W4Mat W,
+    wide_kernel(int N, W4Shape sh, int chunk, const bf* __restrict__ x, W4Mat W,
                 float* __restrict__ y) {
   using Unit = W4Unit<HALF>;
   constexpr int T = NT * 8;
   extern __shared__ __align__(16) unsigned char xs[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  // rows of x are apart by an odd number of 16-byte columns (HALF: of 64-byte ones), so the 8
-  // lanes that read 16 bytes at a time meet no bank twice
+  // the pitch keeps the 8 lanes that read 16 bytes at a time on different banks
   const int pitch = chunk * 2 + (HALF ? 64 : 16);
-  const int tiles = (d_out + kWideRows - 1) / kWideRows;
-  const int chunks = (d_in + chunk - 1) / chunk;
+  const int tiles = (sh.d_out + kWideRows - 1) / kWideRows;
+  const int chunks = (sh.d_in + chunk - 1) / chunk;
   for (int first = 0; first < tiles; first += gridDim.x * warps) {  // a round, same for all CTAs
     const int tile = first + warp * gridDim.x + blockIdx.x;
     const bool mine = tile < tiles;
-    const typename Unit::Src s0(W, d_out, d_in, group, tile * kWideRows, g);
-    const typename Unit::Src s1(W, d_out, d_in, group, tile * kWideRows + 16, g);
+    const typename Unit::Src s0(W, sh, tile * kWideRows, g), s1(W, sh, tile * kWideRows + 16, g);
     float acc[2][NT][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
@@ -357,50 +385,49 @@ __global__ void __launch_bounds__(32 * kWideWarps, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[r][t][i] = 0.f;
     for (int ch = 0; ch < chunks; ++ch) {
-      const int k0 = ch * chunk, cols = min(chunk, d_in - k0);
+      const int k0 = ch * chunk, cols = min(chunk, sh.d_in - k0);
       const int u0 = k0 / 64, u1 = u0 + (cols + 63) / 64;
-      Unit cur[2][kWideBatch], nxt[2][kWideBatch];
-      const auto fetch = [&](Unit (&w)[2][kWideBatch], int u) {
-#pragma unroll
-        for (int b = 0; b < kWideBatch; ++b)
-          if (u + b < u1) {
-            w[0][b].load(s0, u + b, c);
-            w[1][b].load(s1, u + b, c);
-          }
+      Unit w[kWideAhead][2];  // units u0 .. of both tiles, kWideAhead ahead of their use
+      const auto fetch = [&](int slot, int u) {
+        if (u < u1) {
+          w[slot][0].load(s0, sh, u, c);
+          w[slot][1].load(s1, sh, u, c);
+        }
       };
-      if (mine) fetch(cur, u0);
+      if (mine) {
+#pragma unroll
+        for (int i = 0; i < kWideAhead; ++i) fetch(i, u0 + i);
+      }
       if (first == 0 || chunks > 1) {
         if (ch > 0 || first > 0) __syncthreads();  // the chunk before has been read
         const int blocks = (cols + 63) / 64 * 8;   // 8-column blocks, whole units
-        for (int e = threadIdx.x; e < T * blocks; e += blockDim.x) {
-          const int n = e / blocks, b = e % blocks;
-          *reinterpret_cast<uint4*>(xs + n * pitch + b * 16) =
-              w4_order(x8(x, N, d_in, n, k0 + b * 8));
+        for (int n = warp; n < T; n += warps) {
+          const uint32_t dst = smem_addr(xs + n * pitch);
+          const bf* src = x + (int64_t)min(n, N - 1) * sh.d_in + k0;
+          for (int b = lane; b < blocks; b += 32)
+            copy16(dst + b * 16, src + (b * 8 < cols ? b * 8 : 0), n < N && b * 8 < cols);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
       }
       if (!mine) continue;
-      for (int u = u0; u < u1; u += kWideBatch) {
-        if (u + kWideBatch < u1) fetch(nxt, u + kWideBatch);
+      const unsigned char* xb = xs + g * pitch;
+      for (int u = u0; u < u1; u += kWideAhead) {
 #pragma unroll
-        for (int b = 0; b < kWideBatch; ++b) {
-          if (u + b >= u1) break;
-          const typename Unit::A a0 = cur[0][b].operands(), a1 = cur[1][b].operands();
-          const unsigned char* xb = xs + g * pitch;
-          const int o0 = Unit::col((u + b - u0) * 64, c, 0) * 2;
-          const int o1 = Unit::col((u + b - u0) * 64, c, 1) * 2;
+        for (int i = 0; i < kWideAhead; ++i) {
+          if (u + i >= u1) break;
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const uint4 xv[2] = {*reinterpret_cast<const uint4*>(xb + t * 8 * pitch + o0),
-                                 *reinterpret_cast<const uint4*>(xb + t * 8 * pitch + o1)};
-            cur[0][b].mac(acc[0][t], a0, xv);
-            cur[1][b].mac(acc[1][t], a1, xv);
+          for (int j = 0; j < 2; ++j) {
+            const typename Unit::A a0 = w[i][0].operands(j), a1 = w[i][1].operands(j);
+            const unsigned char* xj = xb + Unit::col((u + i - u0) * 64, c, j) * 2;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const uint4 xv = *reinterpret_cast<const uint4*>(xj + t * 8 * pitch);
+              Unit::mac(acc[0][t], a0, xv);
+              Unit::mac(acc[1][t], a1, xv);
+            }
           }
-        }
-#pragma unroll
-        for (int b = 0; b < kWideBatch; ++b) {
-          cur[0][b] = nxt[0][b];
-          cur[1][b] = nxt[1][b];
+          fetch(i, u + i + kWideAhead);
         }
       }
     }
@@ -412,14 +439,14 @@ __global__ void __launch_bounds__(32 * kWideWarps, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int n = t * 8 + 2 * c + (i & 1), o = tile * kWideRows + r * 16 + g + 8 * (i >> 1);
-          if (n < N && o < d_out) y[(int64_t)n * d_out + o] = acc[r][t][i];
+          if (n < N && o < sh.d_out) y[(int64_t)n * sh.d_out + o] = acc[r][t][i];
         }
   }
 }
 
 template <bool HALF, int NT>
-cudaError_t launch_wide(int N, int d_in, int d_out, int group, const bf* x, const W4Mat& W,
-                        float* y, int sm_count, cudaStream_t st) {
+cudaError_t launch_wide(int N, const W4Shape& sh, const bf* x, const W4Mat& W, float* y,
+                        int sm_count, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -432,13 +459,13 @@ cudaError_t launch_wide(int N, int d_in, int d_out, int group, const bf* x, cons
   }
   const int pad = HALF ? 64 : 16;
   const int most = (kWideSmem / (NT * 8) - pad) / 2 / 64 * 64;
-  const int chunk = std::min((d_in + 63) / 64 * 64, most);
-  const int tiles = (d_out + kWideRows - 1) / kWideRows;
+  const int chunk = std::min((sh.d_in + 63) / 64 * 64, most);
+  const int tiles = (sh.d_out + kWideRows - 1) / kWideRows;
   const int per_sm = (tiles + sm_count - 1) / sm_count;
   const int rounds = (per_sm + kWideWarps - 1) / kWideWarps;
   const int warps = (per_sm + rounds - 1) / rounds;
-  wide_kernel<HALF, NT><<<std::min(tiles, sm_count), 32 * warps, (size_t)NT * 8 * (chunk * 2 + pad), st>>>(
-      N, d_in, d_out, group, chunk, x, W, y);
+  wide_kernel<HALF, NT><<<std::min(tiles, sm_count), 32 * warps,
+                          (size_t)NT * 8 * (chunk * 2 + pad), st>>>(N, sh, chunk, x, W, y);
   PKM_COUNT(1);
   return cudaGetLastError();
 }
@@ -457,50 +484,57 @@ int split_of(int d_out, int d_in, int sm_count) {
   return ks;
 }
 
-template <class Unit, class Mat, int NT, Few OUT, int ACT>
-cudaError_t launch(int N, int d_in, int d_out, int group, const bf* x, const Mat& W0,
-                   const Mat& W1, void* out, bool first, int sm_count, cudaStream_t st) {
-  const int ks = split_of(d_out, d_in, sm_count);
+template <class Unit, class Of, int NT, Few OUT, int ACT>
+cudaError_t launch(int N, const typename Of::Shape& sh, const bf* x, const typename Of::Mat& W0,
+                   const typename Of::Mat& W1, void* out, bool first, int sm_count,
+                   cudaStream_t st) {
+  const auto kernel = few_kernel<Unit, typename Of::Mat, typename Of::Shape, NT, OUT, ACT>;
+  const int ks = split_of(sh.d_out, sh.d_in, sm_count);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((d_out + kRows - 1) / kRows * ks));
+  cfg.gridDim = dim3((unsigned)((sh.d_out + kRows - 1) / kRows * ks));
   cfg.blockDim = dim3(kTpb);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ks;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  int n = 0;
+  if (ks > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = ks;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (!first) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = first ? 1 : 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, few_kernel<Unit, Mat, NT, OUT, ACT>, N, d_in,
-                                           d_out, group, ks, x, W0, W1, out, first);
+  cfg.numAttrs = n;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, N, sh, ks, x, W0, W1, out, first);
   PKM_COUNT(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <class Unit, class Mat, Few OUT, int ACT, int MAXT>
-cudaError_t by_tokens(int N, int d_in, int d_out, int group, const bf* x, const Mat& W0,
-                      const Mat& W1, void* out, bool first, int sm_count, cudaStream_t st) {
-  if (N <= 8)
-    return launch<Unit, Mat, 1, OUT, ACT>(N, d_in, d_out, group, x, W0, W1, out, first, sm_count, st);
-  if (N <= 16)
-    return launch<Unit, Mat, 2, OUT, ACT>(N, d_in, d_out, group, x, W0, W1, out, first, sm_count, st);
+template <class Unit, class Of, Few OUT, int ACT, int MAXT>
+cudaError_t by_tokens(int64_t N, const typename Of::Shape& sh, const bf* x,
+                      const typename Of::Mat& W0, const typename Of::Mat& W1, void* out,
+                      bool first, int sm_count, cudaStream_t st) {
+  const int n = (int)N;
+  if (N <= 8) return launch<Unit, Of, 1, OUT, ACT>(n, sh, x, W0, W1, out, first, sm_count, st);
+  if (N <= 16) return launch<Unit, Of, 2, OUT, ACT>(n, sh, x, W0, W1, out, first, sm_count, st);
   if constexpr (MAXT > 16) {
-    if (N <= 32)
-      return launch<Unit, Mat, 4, OUT, ACT>(N, d_in, d_out, group, x, W0, W1, out, first, sm_count, st);
-    return launch<Unit, Mat, 8, OUT, ACT>(N, d_in, d_out, group, x, W0, W1, out, first, sm_count, st);
+    if (N <= 32) return launch<Unit, Of, 4, OUT, ACT>(n, sh, x, W0, W1, out, first, sm_count, st);
+    return launch<Unit, Of, 8, OUT, ACT>(n, sh, x, W0, W1, out, first, sm_count, st);
   }
   return cudaErrorInvalidValue;
 }
 
 template <Few OUT, int ACT>
-cudaError_t w4(int N, int d_in, int d_out, int group, const bf* x, const W4Mat& W0,
+cudaError_t w4(int64_t N, int d_in, int d_out, int group, const bf* x, const W4Mat& W0,
                const W4Mat& W1, void* out, bool first, int sm_count, cudaStream_t st) {
-  return group % 64 ? by_tokens<W4Unit<true>, W4Mat, OUT, ACT, 64>(N, d_in, d_out, group, x, W0, W1,
-                                                                   out, first, sm_count, st)
-                    : by_tokens<W4Unit<false>, W4Mat, OUT, ACT, 64>(N, d_in, d_out, group, x, W0,
-                                                                    W1, out, first, sm_count, st);
+  const W4Shape sh = W4Shape::of(d_in, d_out, group);
+  return group % 64
+             ? by_tokens<W4Unit<true>, W4Of, OUT, ACT, 64>(N, sh, x, W0, W1, out, first, sm_count, st)
+             : by_tokens<W4Unit<false>, W4Of, OUT, ACT, 64>(N, sh, x, W0, W1, out, first, sm_count, st);
 }
 
 }  // namespace
@@ -508,15 +542,14 @@ cudaError_t w4(int N, int d_in, int d_out, int group, const bf* x, const W4Mat& 
 cudaError_t launch_w4_matvec(int64_t N, int d_in, int d_out, int group, const void* x,
                              const W4Mat& W, float* y, int sm_count, cudaStream_t st) {
   const bf* xb = static_cast<const bf*>(x);
-  const int n = (int)N;
-  if (wide_form(N, d_out, sm_count)) {
-    if (group % 64)
-      return N <= 32 ? launch_wide<true, 4>(n, d_in, d_out, group, xb, W, y, sm_count, st)
-                     : launch_wide<true, 8>(n, d_in, d_out, group, xb, W, y, sm_count, st);
-    return N <= 32 ? launch_wide<false, 4>(n, d_in, d_out, group, xb, W, y, sm_count, st)
-                   : launch_wide<false, 8>(n, d_in, d_out, group, xb, W, y, sm_count, st);
-  }
-  return w4<Few::kF32, 0>(n, d_in, d_out, group, xb, W, W, y, true, sm_count, st);
+  if (!wide_form(N, d_out, sm_count))
+    return w4<Few::kF32, 0>(N, d_in, d_out, group, xb, W, W, y, true, sm_count, st);
+  const W4Shape sh = W4Shape::of(d_in, d_out, group);
+  if (group % 64)
+    return N <= 32 ? launch_wide<true, 4>((int)N, sh, xb, W, y, sm_count, st)
+                   : launch_wide<true, 8>((int)N, sh, xb, W, y, sm_count, st);
+  return N <= 32 ? launch_wide<false, 4>((int)N, sh, xb, W, y, sm_count, st)
+                 : launch_wide<false, 8>((int)N, sh, xb, W, y, sm_count, st);
 }
 
 cudaError_t launch_w4_ffn(const FfnPlan& p, int group, const void* x, const W4Mat& Wg,
@@ -524,28 +557,26 @@ cudaError_t launch_w4_ffn(const FfnPlan& p, int group, const void* x, const W4Ma
   const bf* xb = static_cast<const bf*>(x);
   const cudaError_t e =
       p.act == PKM_ACT_GELU
-          ? w4<Few::kGate, PKM_ACT_GELU>((int)p.N, p.d_in, p.d_ff, group, xb, Wg, Wu, ws, true, p.sm_count, st)
-          : w4<Few::kGate, PKM_ACT_SILU>((int)p.N, p.d_in, p.d_ff, group, xb, Wg, Wu, ws, true, p.sm_count, st);
+          ? w4<Few::kGate, PKM_ACT_GELU>(p.N, p.d_in, p.d_ff, group, xb, Wg, Wu, ws, true, p.sm_count, st)
+          : w4<Few::kGate, PKM_ACT_SILU>(p.N, p.d_in, p.d_ff, group, xb, Wg, Wu, ws, true, p.sm_count, st);
   if (e != cudaSuccess) return e;
-  return w4<Few::kBf16, 0>((int)p.N, p.d_ff, p.d_out, group, static_cast<const bf*>(ws), Wd, Wd, y,
+  return w4<Few::kBf16, 0>(p.N, p.d_ff, p.d_out, group, static_cast<const bf*>(ws), Wd, Wd, y,
                            false, p.sm_count, st);
 }
 
 cudaError_t launch_ffn_few(const FfnPlan& p, const void* x, const void* Wg, const void* Wu,
                            const void* Wd, void* y, void* ws, cudaStream_t st) {
-  const bf* xb = static_cast<const bf*>(x);
-  const bf *g = static_cast<const bf*>(Wg), *u = static_cast<const bf*>(Wu),
-           *o = static_cast<const bf*>(Wd);
+  const bf *xb = static_cast<const bf*>(x), *g = static_cast<const bf*>(Wg),
+           *u = static_cast<const bf*>(Wu), *o = static_cast<const bf*>(Wd);
   constexpr int kMost = (int)kFfnFewTokens;
+  const W16Shape in = W16Shape::of(p.d_in, p.d_ff, 0), back = W16Shape::of(p.d_ff, p.d_out, 0);
   const cudaError_t e =
       p.act == PKM_ACT_GELU
-          ? by_tokens<W16Unit, const bf*, Few::kGate, PKM_ACT_GELU, kMost>(
-                (int)p.N, p.d_in, p.d_ff, 0, xb, g, u, ws, true, p.sm_count, st)
-          : by_tokens<W16Unit, const bf*, Few::kGate, PKM_ACT_SILU, kMost>(
-                (int)p.N, p.d_in, p.d_ff, 0, xb, g, u, ws, true, p.sm_count, st);
+          ? by_tokens<W16Unit, W16Of, Few::kGate, PKM_ACT_GELU, kMost>(p.N, in, xb, g, u, ws, true, p.sm_count, st)
+          : by_tokens<W16Unit, W16Of, Few::kGate, PKM_ACT_SILU, kMost>(p.N, in, xb, g, u, ws, true, p.sm_count, st);
   if (e != cudaSuccess) return e;
-  return by_tokens<W16Unit, const bf*, Few::kBf16, 0, kMost>(
-      (int)p.N, p.d_ff, p.d_out, 0, static_cast<const bf*>(ws), o, o, y, false, p.sm_count, st);
+  return by_tokens<W16Unit, W16Of, Few::kBf16, 0, kMost>(p.N, back, static_cast<const bf*>(ws), o, o,
+                                                         y, false, p.sm_count, st);
 }
 
 }  // namespace pkm
