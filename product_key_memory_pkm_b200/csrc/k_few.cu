@@ -20,6 +20,7 @@
 // distributed shared memory.  Every sum has a fixed order.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "ffn_internal.cuh"
 
@@ -30,7 +31,6 @@ using bf = __nv_bfloat16;
 
 constexpr int kWarps = 8, kTpb = 32 * kWarps;
 constexpr int kRows = 16;   // output rows of a CTA
-constexpr int kBatch = 4;   // units a warp has in flight
 
 // (Not volatile: the compiler may interleave independent products.)
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -64,97 +64,90 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint3
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// 8 columns of a token, zeros for no token or no column.
-__device__ __forceinline__ uint4 x8(const bf* x, int64_t N, int d_in, int n, int k) {
-  return n < N && k < d_in ? *reinterpret_cast<const uint4*>(x + (int64_t)n * d_in + k)
-                           : make_uint4(0, 0, 0, 0);
-}
-
 // ------------------------------------------------------------------ weights
 // Weights of one unit for this lane's two rows (g and g + 8 of a tile of 16).
 //
-// 4-bit: a unit is 64 columns.  HALF = false (groups of whole units): the lane holds columns
-// [k0 + 16 c, +16) and one scale serves the unit.  HALF = true (groups of 32, 96, ...): columns
-// [k0 + 8 c, +8) and [k0 + 32 + 8 c, +8), each half with its own scale.
+// 4-bit: a unit is 32 * WORDS columns of one group: 128 where groups are whole multiples of
+// that, else 64, else 32, so that one scale serves it.  The lane holds the 8 * WORDS neighbouring
+// columns from 8 * WORDS * c, as one load.
 struct W4Shape {
   int d_in, d_out, ng;
-  uint32_t magic;  // quotient by a group's length in units (HALF: half units): see group_of
+  uint32_t magic;  // for the quotient by a group's length in units: see group_of
+  static int words(int group) { return group % 128 == 0 ? 4 : group % 64 == 0 ? 2 : 1; }
   static W4Shape of(int d_in, int d_out, int group) {
-    const uint32_t per = (uint32_t)(group % 64 ? group / 32 : group / 64);
+    const uint32_t per = (uint32_t)(group / (32 * words(group)));
     return W4Shape{d_in, d_out, (d_in + group - 1) / group,
                    per == 1 ? 0u : (uint32_t)(((uint64_t)1 << 32) / per + 1)};
   }
   // i / per for i < 2^15, per <= 2^15: the error of magic, below per, adds i * per / 2^32 < 1/4
   __device__ int group_of(int i) const { return magic ? (int)__umulhi((uint32_t)i, magic) : i; }
 };
-template <bool HALF>
+template <int WORDS>
 struct W4Unit {
-  static constexpr int kCols = 64;
-  static constexpr int kScales = HALF ? 2 : 1;
-  uint32_t w[2][2];  // [row][word]
-  bf s[2][kScales];
+  static constexpr int kCols = 32 * WORDS, kWords = WORDS;
+  uint32_t w[2][WORDS];
+  uint32_t s[2];  // the scales' bits, not packed: packing would wait for the loads
 
   struct Src {
     const uint8_t* codes;
-    const bf* scale;
+    const unsigned short* scale;
     int next_c, next_s;  // from row g to row g + 8, in bytes and in scales
-    __device__ Src(const W4Mat& W, const W4Shape& sh, int o0, int g) {
+    __device__ Src(const W4Mat& W, const W4Shape& sh, int o0, int g, int c) {
       // rows past the last are read as the last and not stored
-      const int64_t o = min(o0 + g, sh.d_out - 1), p = min(o0 + g + 8, sh.d_out - 1);
-      codes = W.codes + o * (sh.d_in / 2);
-      scale = W.scale + o * sh.ng;
-      next_c = (int)(p - o) * (sh.d_in / 2);
-      next_s = (int)(p - o) * sh.ng;
+      const int64_t o = min(o0 + g, sh.d_out - 1);
+      const int to = min(o0 + g + 8, sh.d_out - 1) - (int)o;
+      codes = W.codes + o * (sh.d_in / 2) + 4 * WORDS * c;
+      scale = reinterpret_cast<const unsigned short*>(W.scale) + o * sh.ng;
+      next_c = to * (sh.d_in / 2);
+      next_s = to * sh.ng;
     }
   };
-  __device__ static int col(int k0, int c, int j) {
-    return HALF ? k0 + 32 * j + 8 * c : k0 + 16 * c + 8 * j;
-  }
+  __device__ static int col(int u, int c, int j) { return u * kCols + 8 * WORDS * c + 8 * j; }
   __device__ void load(const Src& S, const W4Shape& sh, int u, int c) {
-    const int k0 = u * kCols;
+    // a lane past the row's end reads within the row: its x is zero, and no code is NaN
+    const int at = u * (kCols / 2);
+    const uint8_t* p = S.codes + (col(u, c, 0) < sh.d_in ? at : -4 * WORDS * c);
+    const unsigned short* q = S.scale + sh.group_of(u);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const uint8_t* row = S.codes + (r ? S.next_c : 0);
-      const bf* sc = S.scale + (r ? S.next_s : 0);
-      if (HALF) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int k = col(k0, c, j);
-          w[r][j] = k < sh.d_in ? __ldg(reinterpret_cast<const uint32_t*>(row + k / 2)) : 0u;
-          s[r][kScales * j / 2] = k0 + 32 * j < sh.d_in ? sc[sh.group_of(2 * u + j)] : bf(0.f);
-        }
+      if constexpr (WORDS == 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+        w[r][0] = v.x; w[r][1] = v.y; w[r][2] = v.z; w[r][3] = v.w;
+      } else if constexpr (WORDS == 2) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        w[r][0] = v.x; w[r][1] = v.y;
       } else {
-        const int k = col(k0, c, 0);
-        const uint2 q = k < sh.d_in ? __ldg(reinterpret_cast<const uint2*>(row + k / 2))
-                                    : make_uint2(0u, 0u);
-        w[r][0] = q.x;
-        w[r][1] = q.y;
-        s[r][0] = sc[sh.group_of(u)];
+        w[r][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
       }
+      s[r] = __ldg(q);
+      p += S.next_c;
+      q += S.next_s;
     }
   }
-  // The A operands and scales of word j.
+  // The A operands of word j.
   struct A {
     uint32_t g[4], h[4];
-    float sg, sh;
   };
   __device__ A operands(int j) const {
     A o;
     w4_pairs(w[0][j], o.g);
     w4_pairs(w[1][j], o.h);
-    o.sg = to_f32(s[0][kScales * j / 2]);
-    o.sh = to_f32(s[1][kScales * j / 2]);
     return o;
   }
-  // acc += the word's products with 8 tokens, x their columns
-  __device__ static void mac(float (&acc)[4], const A& o, const uint4& x) {
-    float t[4];
-    mma16816_first(t, o.g[0], o.h[0], o.g[1], o.h[1], x.x, x.y);
+  // t (+)= word j's products with 8 tokens, x their columns; after the last word, acc += scale t
+  __device__ static void mac(float (&t)[4], const A& o, const uint4& x, int j) {
+    if (j == 0)
+      mma16816_first(t, o.g[0], o.h[0], o.g[1], o.h[1], x.x, x.y);
+    else
+      mma16816(t, o.g[0], o.h[0], o.g[1], o.h[1], x.x, x.y);
     mma16816(t, o.g[2], o.h[2], o.g[3], o.h[3], x.z, x.w);
-    acc[0] = fmaf(o.sg, t[0], acc[0]);
-    acc[1] = fmaf(o.sg, t[1], acc[1]);
-    acc[2] = fmaf(o.sh, t[2], acc[2]);
-    acc[3] = fmaf(o.sh, t[3], acc[3]);
+  }
+  __device__ void close(float (&acc)[4], const float (&t)[4]) const {
+    const float sg = __uint_as_float(s[0] << 16), sh = __uint_as_float(s[1] << 16);
+    acc[0] = fmaf(sg, t[0], acc[0]);
+    acc[1] = fmaf(sg, t[1], acc[1]);
+    acc[2] = fmaf(sh, t[2], acc[2]);
+    acc[3] = fmaf(sh, t[3], acc[3]);
   }
 };
 
@@ -164,37 +157,42 @@ struct W16Shape {
   static W16Shape of(int d_in, int d_out, int) { return W16Shape{d_in, d_out}; }
 };
 struct W16Unit {
-  static constexpr int kCols = 64;
+  static constexpr int kCols = 64, kWords = 2;
   uint4 w[2][2];  // [row][half]
 
   struct Src {
     const bf* row;
     int64_t next;
-    __device__ Src(const bf* W, const W16Shape& sh, int o0, int g) {
+    __device__ Src(const bf* W, const W16Shape& sh, int o0, int g, int c) {
       const int64_t o = min(o0 + g, sh.d_out - 1), p = min(o0 + g + 8, sh.d_out - 1);
-      row = W + o * sh.d_in;
+      row = W + o * sh.d_in + 8 * c;
       next = (p - o) * sh.d_in;
     }
   };
-  __device__ static int col(int k0, int c, int j) { return k0 + 32 * j + 8 * c; }
+  __device__ static int col(int u, int c, int j) { return u * kCols + 32 * j + 8 * c; }
   __device__ void load(const Src& S, const W16Shape& sh, int u, int c) {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int k = col(u * kCols, c, j);
-        w[r][j] = k < sh.d_in
-                      ? __ldcs(reinterpret_cast<const uint4*>(S.row + (r ? S.next : 0) + k))
+      for (int j = 0; j < 2; ++j)
+        w[r][j] = col(u, c, j) < sh.d_in
+                      ? __ldcs(reinterpret_cast<const uint4*>(S.row + (r ? S.next : 0) + u * kCols + 32 * j))
                       : make_uint4(0, 0, 0, 0);
-      }
   }
   struct A {
     uint4 g, h;
   };
   __device__ A operands(int j) const { return A{w[0][j], w[1][j]}; }
-  __device__ static void mac(float (&acc)[4], const A& o, const uint4& x) {
-    mma16816(acc, o.g.x, o.h.x, o.g.y, o.h.y, x.x, x.y);
-    mma16816(acc, o.g.z, o.h.z, o.g.w, o.h.w, x.z, x.w);
+  __device__ static void mac(float (&t)[4], const A& o, const uint4& x, int j) {
+    if (j == 0)
+      mma16816_first(t, o.g.x, o.h.x, o.g.y, o.h.y, x.x, x.y);
+    else
+      mma16816(t, o.g.x, o.h.x, o.g.y, o.h.y, x.x, x.y);
+    mma16816(t, o.g.z, o.h.z, o.g.w, o.h.w, x.z, x.w);
+  }
+  __device__ void close(float (&acc)[4], const float (&t)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] += t[i];
   }
 };
 struct W4Of {
@@ -225,122 +223,174 @@ __device__ __forceinline__ void cluster_sync() {
 enum class Few { kF32, kBf16, kGate };  // y fp32, y bf16, or h = act(first) * second in bf16
 
 // NT: tokens in blocks of 8.  GATE uses both matrices, the others the first.
-template <class Unit, class Mat, class Shape, int NT, Few OUT, int ACT>
-__global__ void __launch_bounds__(kTpb) few_kernel(int N, Shape sh, int ks,
-                                                   const bf* __restrict__ x, Mat W0, Mat W1,
-                                                   void* __restrict__ out, bool first) {
+// M: blocks of 16 rows of a CTA's tile: one, two (a matrix of many rows: x is read once for
+// both), or for the gate one of each matrix.
+// Units a warp has in flight, and the CTAs an SM holds: few units and several CTAs, so that
+// the CTAs of one grid are resident together and none waits for another's last loads (one
+// token, 1600 x 6400 x 1600 in bf16: 18 us; two units and 2 CTAs 24, four units and 1 CTA 32).
+#ifndef FEW_B
+#define FEW_B 2
+#define FEW_C 3
+#endif
+template <class Unit, int M, int NT>
+struct Depth {
+  static constexpr int batch = M * NT > 4 ? 1 : (FEW_B * 4 / M / Unit::kWords > 0 ? FEW_B * 4 / M / Unit::kWords : 1), ctas = M * NT > 2 ? 1 : FEW_C;
+};
+template <int M, int NT>
+struct Depth<W16Unit, M, NT> {
+  static constexpr int batch = M == 2 ? 1 : 2, ctas = M * NT > 2 ? 2 : 3;
+};
+
+template <class Unit, class Mat, class Shape, int M, int NT, Few OUT, int ACT>
+__global__ void __launch_bounds__(kTpb, Depth<Unit, M, NT>::ctas)
+    few_kernel(int N, Shape sh, int ks, const bf* __restrict__ x, Mat W0, Mat W1,
+               void* __restrict__ out, bool first) {
   const int d_in = sh.d_in, d_out = sh.d_out;
-  constexpr int M = OUT == Few::kGate ? 2 : 1;
-  constexpr int T = NT * 8;
+  constexpr int kTileRows = OUT == Few::kGate ? kRows : M * kRows;
+  constexpr int kNext = OUT == Few::kGate ? 0 : kRows;  // rows from the first block to the second
+  constexpr int T = NT * 8, kBatch = Depth<Unit, M, NT>::batch;
   // a slot per warp, or per two warps where 8 would pass the static limit of 48 KiB
   constexpr int kSlots = M * NT <= 8 ? kWarps : kWarps / 2;
   __shared__ float part[M][kSlots][T][kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int rank = ks > 1 ? (int)blockIdx.x % ks : 0;
-  const int o0 = (int)blockIdx.x / ks * kRows;
+  const int tiles = (d_out + kTileRows - 1) / kTileRows, stride = (int)gridDim.x / ks;
   const int units = (d_in + Unit::kCols - 1) / Unit::kCols;
-  const int per = (units + kWarps * ks - 1) / (kWarps * ks);
-  const int u0 = (rank * kWarps + warp) * per, u1 = min(units, u0 + per);
+  const int step = kWarps * ks, u0 = rank * kWarps + warp;  // units u0, u0 + step, ...
+  int tile = (int)blockIdx.x / ks;
 
-  const typename Unit::Src s0(W0, sh, o0, g), s1(M == 2 ? W1 : W0, sh, o0, g);
-  float acc[M][NT][4];
-#pragma unroll
-  for (int m = 0; m < M; ++m)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][t][i] = 0.f;
-
+  typename Unit::Src s0(W0, sh, tile * kTileRows, g, c), s1(W1, sh, tile * kTileRows + kNext, g, c);
   Unit w[M][kBatch];
   const auto fetch = [&](int u) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b)
-      if (u + b < u1) {
-        w[0][b].load(s0, sh, u + b, c);
-        if (M == 2) w[M - 1][b].load(s1, sh, u + b, c);
+      if (u + b * step < units) {
+        w[0][b].load(s0, sh, u + b * step, c);
+        if (M == 2) w[M - 1][b].load(s1, sh, u + b * step, c);
       }
   };
+  // Blocks past the last token repeat it: a column of the products that is not stored may hold
+  // anything, since columns do not mix.
+  const bf* xp[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xp[n] = x + (int64_t)min(n * 8 + g, N - 1) * d_in;
+
   // weights do not depend on the kernel before, x of the second product does
-  if (u0 < u1) fetch(u0);
+  fetch(u0);
   if (first)
     allow_dependent_launch();
   else
     grid_dependency_wait();
-  for (int u = u0; u < u1; u += kBatch) {
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (u + b >= u1) break;
-      const int k0 = (u + b) * Unit::kCols;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        typename Unit::A a[M];
-#pragma unroll
-        for (int m = 0; m < M; ++m) a[m] = w[m][b].operands(j);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const uint4 xv = x8(x, N, d_in, t * 8 + g, Unit::col(k0, c, j));
-#pragma unroll
-          for (int m = 0; m < M; ++m) Unit::mac(acc[m][t], a[m], xv);
-        }
-      }
-    }
-    if (u + kBatch < u1) fetch(u + kBatch);
-  }
-
-  // rows g, g + 8 and tokens 2c, 2c + 1 of each block of 8
-  const auto leave = [&](bool add) {
+  for (; tile < tiles; tile += stride) {
+    const int o0 = tile * kTileRows;
+    float acc[M][NT][4];
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float* p = &part[m][warp % kSlots][t * 8 + 2 * c + (i & 1)][g + 8 * (i >> 1)];
-          *p = add ? *p + acc[m][t][i] : acc[m][t][i];
+        for (int i = 0; i < 4; ++i) acc[m][t][i] = 0.f;
+    for (int u = u0; u < units; u += kBatch * step) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (u + b * step >= units) break;
+        const int v = u + b * step;
+        float t[M][NT][4];
+        const auto products = [&](auto edge) {  // edge: the row ends within the unit
+#pragma unroll
+          for (int j = 0; j < Unit::kWords; ++j) {
+            typename Unit::A a[M];
+#pragma unroll
+            for (int m = 0; m < M; ++m) a[m] = w[m][b].operands(j);
+            const int k = Unit::col(v, c, j);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              uint4 xv = make_uint4(0, 0, 0, 0);
+              if (!decltype(edge)::value || k < d_in) xv = *reinterpret_cast<const uint4*>(xp[n] + k);
+#pragma unroll
+              for (int m = 0; m < M; ++m) Unit::mac(t[m][n], a[m], xv, j);
+            }
+          }
+        };
+        if ((v + 1) * Unit::kCols > d_in) products(std::true_type{}); else products(std::false_type{});
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) w[m][b].close(acc[m][n], t[m][n]);
+      }
+      fetch(u + kBatch * step);
+    }
+    if (tile + stride < tiles) {  // the next tile's first weights travel beside this one's sums
+      s0 = typename Unit::Src(W0, sh, o0 + stride * kTileRows, g, c);
+      s1 = typename Unit::Src(W1, sh, o0 + stride * kTileRows + kNext, g, c);
+      fetch(u0);
+    }
+
+    // rows g, g + 8 and tokens 2c, 2c + 1 of each block of 8
+    const auto leave = [&](bool add) {
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float* p = &part[m][warp % kSlots][t * 8 + 2 * c + (i & 1)][g + 8 * (i >> 1)];
+            *p = add ? *p + acc[m][t][i] : acc[m][t][i];
+          }
+    };
+    if (warp < kSlots) leave(false);
+    __syncthreads();
+    if (kSlots < kWarps) {
+      if (warp >= kSlots) leave(true);
+      __syncthreads();
+    }
+    const auto own_sum = [&](int m, int n, int r) {
+      float s = part[m][0][n][r];
+#pragma unroll
+      for (int q = 1; q < kSlots; ++q) s += part[m][q][n][r];
+      return s;
+    };
+    if (ks > 1) {
+      for (int e = threadIdx.x; e < M * N * kRows; e += kTpb) {
+        const int m = e / (N * kRows), n = e / kRows % N, r = e % kRows;
+        part[m][0][n][r] = own_sum(m, n, r);
+      }
+      __syncwarp();
+      cluster_sync();
+    }
+    // each CTA of a cluster finishes its share of the elements
+    for (int e = threadIdx.x + rank * kTpb; e < N * kRows; e += kTpb * ks) {
+      const int n = e / kRows, r = e % kRows;
+      float s[M];
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        if (ks > 1) {
+          const uint32_t a = smem_addr(&part[m][0][n][r]);
+          s[m] = peer_load(a, 0);
+          for (int q = 1; q < ks; ++q) s[m] += peer_load(a, q);
+        } else {
+          s[m] = own_sum(m, n, r);
         }
-  };
-  if (warp < kSlots) leave(false);
-  __syncthreads();
-  if (kSlots < kWarps) {
-    if (warp >= kSlots) leave(true);
-    __syncthreads();
-  }
-  for (int e = threadIdx.x; e < M * T * kRows; e += kTpb) {
-    const int m = e / (T * kRows), n = e / kRows % T, r = e % kRows;
-    float s = part[m][0][n][r];
+      }
+      if (OUT == Few::kGate) s[0] = act_fn<ACT>(s[0]) * s[M - 1];
 #pragma unroll
-    for (int q = 1; q < kSlots; ++q) s += part[m][q][n][r];
-    part[m][0][n][r] = s;
-  }
-  if (ks > 1) {
-    __syncwarp();
-    cluster_sync();
-  } else {
-    __syncthreads();
-  }
-  // each CTA of a cluster finishes its share of the elements
-  for (int e = threadIdx.x + rank * kTpb; e < N * kRows; e += kTpb * ks) {
-    const int n = e / kRows, r = e % kRows;
-    float s[M];
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-      s[m] = part[m][0][n][r];
-      if (ks > 1) {
-        const uint32_t a = smem_addr(&part[m][0][n][r]);
-        s[m] = peer_load(a, 0);
-        for (int q = 1; q < ks; ++q) s[m] += peer_load(a, q);
+      for (int m = 0; m < (OUT == Few::kGate ? 1 : M); ++m) {
+        const int o = o0 + m * kRows + r;
+        const int64_t at = (int64_t)n * d_out + o;
+        if (o >= d_out) continue;
+        if (OUT == Few::kF32)
+          static_cast<float*>(out)[at] = s[m];
+        else
+          static_cast<bf*>(out)[at] = __float2bfloat16_rn(s[m]);
       }
     }
-    if (o0 + r >= d_out) continue;
-    const int64_t at = (int64_t)n * d_out + o0 + r;
-    if (OUT == Few::kF32) static_cast<float*>(out)[at] = s[0];
-    if (OUT == Few::kBf16) static_cast<bf*>(out)[at] = __float2bfloat16_rn(s[0]);
-    if (OUT == Few::kGate)
-      static_cast<bf*>(out)[at] = __float2bfloat16_rn(act_fn<ACT>(s[0]) * s[M - 1]);
-  }
-  if (ks > 1) {  // a CTA's shared memory outlives its peers' reads
-    __syncwarp();
-    cluster_sync();
+    // the sums are read before they are written again, or before a CTA of the cluster leaves
+    if (ks > 1) {
+      __syncwarp();
+      cluster_sync();
+    } else if (tile + stride < tiles) {
+      __syncthreads();
+    }
   }
 }
 
@@ -360,23 +410,27 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool has) 
                : "memory");
 }
 
-template <bool HALF, int NT>
+__host__ __device__ constexpr int wide_pad(int words) { return words == 1 ? 64 : words == 2 ? 16 : 32; }
+
+template <int WORDS, int NT>
 __global__ void __launch_bounds__(32 * kWideWarps, 1)
     wide_kernel(int N, W4Shape sh, int chunk, const bf* __restrict__ x, W4Mat W,
                 float* __restrict__ y) {
-  using Unit = W4Unit<HALF>;
+  using Unit = W4Unit<WORDS>;
   constexpr int T = NT * 8;
   extern __shared__ __align__(16) unsigned char xs[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  // the pitch keeps the 8 lanes that read 16 bytes at a time on different banks
-  const int pitch = chunk * 2 + (HALF ? 64 : 16);
+  // the 8 lanes that read 16 bytes at a time are two rows' four columns 16 * WORDS bytes apart:
+  // a pitch of 64, 16, 32 bytes past a multiple of 128 keeps them on different banks for 1 and 2
+  // words, and to two turns for 4
+  const int pitch = chunk * 2 + wide_pad(WORDS);
   const int tiles = (sh.d_out + kWideRows - 1) / kWideRows;
   const int chunks = (sh.d_in + chunk - 1) / chunk;
   for (int first = 0; first < tiles; first += gridDim.x * warps) {  // a round, same for all CTAs
     const int tile = first + warp * gridDim.x + blockIdx.x;
     const bool mine = tile < tiles;
-    const typename Unit::Src s0(W, sh, tile * kWideRows, g), s1(W, sh, tile * kWideRows + 16, g);
+    const typename Unit::Src s0(W, sh, tile * kWideRows, g, c), s1(W, sh, tile * kWideRows + 16, g, c);
     float acc[2][NT][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
@@ -386,7 +440,7 @@ __global__ void __launch_bounds__(32 * kWideWarps, 1)
         for (int i = 0; i < 4; ++i) acc[r][t][i] = 0.f;
     for (int ch = 0; ch < chunks; ++ch) {
       const int k0 = ch * chunk, cols = min(chunk, sh.d_in - k0);
-      const int u0 = k0 / 64, u1 = u0 + (cols + 63) / 64;
+      const int u0 = k0 / Unit::kCols, u1 = u0 + (cols + Unit::kCols - 1) / Unit::kCols;
       Unit w[kWideAhead][2];  // units u0 .. of both tiles, kWideAhead ahead of their use
       const auto fetch = [&](int slot, int u) {
         if (u < u1) {
@@ -400,7 +454,7 @@ __global__ void __launch_bounds__(32 * kWideWarps, 1)
       }
       if (first == 0 || chunks > 1) {
         if (ch > 0 || first > 0) __syncthreads();  // the chunk before has been read
-        const int blocks = (cols + 63) / 64 * 8;   // 8-column blocks, whole units
+        const int blocks = (u1 - u0) * (Unit::kCols / 8);  // 8-column blocks, whole units
         for (int n = warp; n < T; n += warps) {
           const uint32_t dst = smem_addr(xs + n * pitch);
           const bf* src = x + (int64_t)min(n, N - 1) * sh.d_in + k0;
@@ -416,16 +470,22 @@ __global__ void __launch_bounds__(32 * kWideWarps, 1)
 #pragma unroll
         for (int i = 0; i < kWideAhead; ++i) {
           if (u + i >= u1) break;
+          float p[2][NT][4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < WORDS; ++j) {
             const typename Unit::A a0 = w[i][0].operands(j), a1 = w[i][1].operands(j);
-            const unsigned char* xj = xb + Unit::col((u + i - u0) * 64, c, j) * 2;
+            const unsigned char* xj = xb + Unit::col(u + i - u0, c, j) * 2;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               const uint4 xv = *reinterpret_cast<const uint4*>(xj + t * 8 * pitch);
-              Unit::mac(acc[0][t], a0, xv);
-              Unit::mac(acc[1][t], a1, xv);
+              Unit::mac(p[0][t], a0, xv, j);
+              Unit::mac(p[1][t], a1, xv, j);
             }
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            w[i][0].close(acc[0][t], p[0][t]);
+            w[i][1].close(acc[1][t], p[1][t]);
           }
           fetch(i, u + i + kWideAhead);
         }
@@ -444,7 +504,7 @@ __global__ void __launch_bounds__(32 * kWideWarps, 1)
   }
 }
 
-template <bool HALF, int NT>
+template <int WORDS, int NT>
 cudaError_t launch_wide(int N, const W4Shape& sh, const bf* x, const W4Mat& W, float* y,
                         int sm_count, cudaStream_t st) {
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
@@ -452,19 +512,19 @@ cudaError_t launch_wide(int N, const W4Shape& sh, const bf* x, const W4Mat& W, f
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!(ready.load(std::memory_order_acquire) >> dev & 1)) {
-    e = cudaFuncSetAttribute(wide_kernel<HALF, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(wide_kernel<WORDS, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kWideSmem);
     if (e != cudaSuccess) return e;
     ready.fetch_or((uint64_t)1 << dev, std::memory_order_release);
   }
-  const int pad = HALF ? 64 : 16;
-  const int most = (kWideSmem / (NT * 8) - pad) / 2 / 64 * 64;
-  const int chunk = std::min((sh.d_in + 63) / 64 * 64, most);
+  const int pad = wide_pad(WORDS);
+  const int most = (kWideSmem / (NT * 8) - pad) / 2 / 128 * 128;
+  const int chunk = std::min((sh.d_in + 127) / 128 * 128, most);
   const int tiles = (sh.d_out + kWideRows - 1) / kWideRows;
   const int per_sm = (tiles + sm_count - 1) / sm_count;
   const int rounds = (per_sm + kWideWarps - 1) / kWideWarps;
   const int warps = (per_sm + rounds - 1) / rounds;
-  wide_kernel<HALF, NT><<<std::min(tiles, sm_count), 32 * warps,
+  wide_kernel<WORDS, NT><<<std::min(tiles, sm_count), 32 * warps,
                           (size_t)NT * 8 * (chunk * 2 + pad), st>>>(N, sh, chunk, x, W, y);
   PKM_COUNT(1);
   return cudaGetLastError();
@@ -477,21 +537,24 @@ bool wide_form(int64_t N, int d_out, int sm_count) {
 
 // CTAs of a cluster along k: more while the grid leaves SMs empty and every warp still has
 // two units.
-int split_of(int d_out, int d_in, int sm_count) {
-  const int tiles = (d_out + kRows - 1) / kRows, units = (d_in + 63) / 64;
+int split_of(int tiles, int d_in, int unit, int sm_count) {
+  const int units = (d_in + unit - 1) / unit;
   int ks = 1;
   while (ks < 4 && tiles * ks < 2 * sm_count && units >= 2 * kWarps * 2 * ks) ks *= 2;
   return ks;
 }
 
-template <class Unit, class Of, int NT, Few OUT, int ACT>
-cudaError_t launch(int N, const typename Of::Shape& sh, const bf* x, const typename Of::Mat& W0,
+template <class Unit, class Of, int M, int NT, Few OUT, int ACT>
+cudaError_t launch_m(int N, const typename Of::Shape& sh, const bf* x, const typename Of::Mat& W0,
                    const typename Of::Mat& W1, void* out, bool first, int sm_count,
                    cudaStream_t st) {
-  const auto kernel = few_kernel<Unit, typename Of::Mat, typename Of::Shape, NT, OUT, ACT>;
-  const int ks = split_of(sh.d_out, sh.d_in, sm_count);
+  const auto kernel = few_kernel<Unit, typename Of::Mat, typename Of::Shape, M, NT, OUT, ACT>;
+  constexpr int kTileRows = OUT == Few::kGate ? kRows : M * kRows;
+  const int tiles = (sh.d_out + kTileRows - 1) / kTileRows;
+  const int ks = split_of(tiles, sh.d_in, Unit::kCols, sm_count);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((sh.d_out + kRows - 1) / kRows * ks));
+  constexpr int kCtas = Depth<Unit, M, NT>::ctas;
+  cfg.gridDim = dim3((unsigned)(std::min(tiles, std::max(1, kCtas * sm_count / ks)) * ks));
   cfg.blockDim = dim3(kTpb);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -514,6 +577,17 @@ cudaError_t launch(int N, const typename Of::Shape& sh, const bf* x, const typen
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Two blocks of rows per tile where even so every SM gets several tiles.
+template <class Unit, class Of, int NT, Few OUT, int ACT>
+cudaError_t launch(int N, const typename Of::Shape& sh, const bf* x, const typename Of::Mat& W0,
+                   const typename Of::Mat& W1, void* out, bool first, int sm_count,
+                   cudaStream_t st) {
+  if (OUT == Few::kGate || (NT <= 2 && sh.d_out >= 2 * kRows * 4 * sm_count))
+    return launch_m<Unit, Of, 2, NT, OUT, ACT>(N, sh, x, W0, W1, out, first, sm_count, st);
+  return launch_m<Unit, Of, OUT == Few::kGate ? 2 : 1, NT, OUT, ACT>(N, sh, x, W0, W1, out, first,
+                                                                    sm_count, st);
+}
+
 template <class Unit, class Of, Few OUT, int ACT, int MAXT>
 cudaError_t by_tokens(int64_t N, const typename Of::Shape& sh, const bf* x,
                       const typename Of::Mat& W0, const typename Of::Mat& W1, void* out,
@@ -532,9 +606,18 @@ template <Few OUT, int ACT>
 cudaError_t w4(int64_t N, int d_in, int d_out, int group, const bf* x, const W4Mat& W0,
                const W4Mat& W1, void* out, bool first, int sm_count, cudaStream_t st) {
   const W4Shape sh = W4Shape::of(d_in, d_out, group);
-  return group % 64
-             ? by_tokens<W4Unit<true>, W4Of, OUT, ACT, 64>(N, sh, x, W0, W1, out, first, sm_count, st)
-             : by_tokens<W4Unit<false>, W4Of, OUT, ACT, 64>(N, sh, x, W0, W1, out, first, sm_count, st);
+  switch (W4Shape::words(group)) {
+    case 4: return by_tokens<W4Unit<4>, W4Of, OUT, ACT, 64>(N, sh, x, W0, W1, out, first, sm_count, st);
+    case 2: return by_tokens<W4Unit<2>, W4Of, OUT, ACT, 64>(N, sh, x, W0, W1, out, first, sm_count, st);
+    default: return by_tokens<W4Unit<1>, W4Of, OUT, ACT, 64>(N, sh, x, W0, W1, out, first, sm_count, st);
+  }
+}
+
+template <int WORDS>
+cudaError_t wide(int N, const W4Shape& sh, const bf* x, const W4Mat& W, float* y, int sm_count,
+                 cudaStream_t st) {
+  return N <= 32 ? launch_wide<WORDS, 4>(N, sh, x, W, y, sm_count, st)
+                 : launch_wide<WORDS, 8>(N, sh, x, W, y, sm_count, st);
 }
 
 }  // namespace
@@ -545,11 +628,11 @@ cudaError_t launch_w4_matvec(int64_t N, int d_in, int d_out, int group, const vo
   if (!wide_form(N, d_out, sm_count))
     return w4<Few::kF32, 0>(N, d_in, d_out, group, xb, W, W, y, true, sm_count, st);
   const W4Shape sh = W4Shape::of(d_in, d_out, group);
-  if (group % 64)
-    return N <= 32 ? launch_wide<true, 4>((int)N, sh, xb, W, y, sm_count, st)
-                   : launch_wide<true, 8>((int)N, sh, xb, W, y, sm_count, st);
-  return N <= 32 ? launch_wide<false, 4>((int)N, sh, xb, W, y, sm_count, st)
-                 : launch_wide<false, 8>((int)N, sh, xb, W, y, sm_count, st);
+  switch (W4Shape::words(group)) {
+    case 4: return wide<4>((int)N, sh, xb, W, y, sm_count, st);
+    case 2: return wide<2>((int)N, sh, xb, W, y, sm_count, st);
+    default: return wide<1>((int)N, sh, xb, W, y, sm_count, st);
+  }
 }
 
 cudaError_t launch_w4_ffn(const FfnPlan& p, int group, const void* x, const W4Mat& Wg,
