@@ -43,6 +43,9 @@ pkm_status validate_sizes(const pkm_ffn_dims* d) {
   if ((d->flags & PKM_F_FP32) && (d->flags & PKM_FFN_GRAD_BF16)) return PKM_ERR_INVALID_ARG;
   if (d->d_in > kMaxWidth || d->d_ff > kMaxWidth || d->d_out > kMaxWidth || d->N > kMaxTokens)
     return PKM_ERR_UNSUPPORTED;
+  // tiles are counted in 32 bits
+  if (d->N * (int64_t)std::max(d->d_in, std::max(d->d_ff, d->d_out)) > (int64_t)1 << 44)
+    return PKM_ERR_UNSUPPORTED;
   if ((d->flags & (PKM_F_FP32 | PKM_F_SIMT)) && d->N > kMaxTokensSimt) return PKM_ERR_UNSUPPORTED;
   return PKM_OK;
 }

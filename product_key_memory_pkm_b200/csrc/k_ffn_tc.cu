@@ -56,6 +56,21 @@ __device__ __forceinline__ void stage_f32(unsigned char* stg, int lane, const ui
   for (int v = 0; v < 8; ++v)
     s[v ^ (lane & 7)] = make_uint4(r[4 * v], r[4 * v + 1], r[4 * v + 2], r[4 * v + 3]);
 }
+// The piece transposed: its column j becomes row j of the staged tile, 32 lanes side by side (the
+// swizzles of the two above).
+template <bool F32>
+__device__ __forceinline__ void stage_transposed(unsigned char* stg, int lane,
+                                                 const uint32_t (&r)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (F32)
+      *reinterpret_cast<uint32_t*>(stg + j * 128 + (((lane >> 2) ^ (j & 7)) << 4) +
+                                   (lane & 3) * 4) = r[j];
+    else
+      *reinterpret_cast<bf*>(stg + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) +
+                             (lane & 7) * 2) = __float2bfloat16_rn(__uint_as_float(r[j]));
+  }
+}
 // Shared -> global tile addition in fp32 (every output element has one writer per call).
 __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, const void* src, int x, int y) {
   asm volatile(
@@ -64,39 +79,79 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, const void* s
       "r"(smem_u32(src)), "r"(x), "r"(y)
       : "memory");
 }
-// The staging bytes may be written again: the warp's earlier stores have read them.
-__device__ __forceinline__ void staging_free(int lane) {
-  if (lane == 0) bulk_wait_read_all();
+// The next set of staging bytes, once the stores of the piece before last have read it (every
+// piece is one group of stores).
+__device__ __forceinline__ unsigned char* staging_next(PairEpi& e) {
+  if (e.lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
   __syncwarp();
+  unsigned char* s = e.stg + e.turn * (kPairStg / 2);
+  e.turn ^= 1;
+  return s;
 }
 __device__ __forceinline__ void staging_ready() {
   fence_proxy_async_smem();
   __syncwarp();
 }
 
-// Tiles walk the output in bands of kBand row tiles, all column tiles of a band before the
-// next, so the tiles in flight at one time share rows of A and of B in L2.
-constexpr int kBand = 8;
-__device__ __forceinline__ void band_tile(int u, int m_tiles, int n_tiles, int* mt, int* nt) {
-  const int per = kBand * n_tiles, b = u / per, r = u % per;
-  const int rows = min(kBand, m_tiles - b * kBand);
-  *mt = b * kBand + r % rows;
-  *nt = r / rows;
-}
-
-// K-major operand half: 128 rows from `row`; MN-major: two 64 x 64 boxes from column `row`.
+// A CTA's 128 rows of A.  K-major: one box of 128 rows x 64 k; MN-major: two blocks of 64
+// columns x 64 k.
 template <int MN>
-__device__ __forceinline__ void load_half(const CUtensorMap* map, void* s, int row, int k,
-                                          uint64_t* bar) {
-  if (MN) {
+__device__ __forceinline__ void load_a(const PairMaps& m, const CUtensorMap* map, void* s, int row,
+                                       int k, uint64_t* bar) {
+  if (!MN) {
+    pair_load_2d(s, map, k, row, bar);
+  } else if (m.a3) {
+    pair_load_3d(s, map, 0, k, row >> 6, bar);
+  } else {
     pair_load_2d(s, map, row, k, bar);
     pair_load_2d(static_cast<unsigned char*>(s) + 8192, map, row + 64, k, bar);
-  } else {
-    pair_load_2d(s, map, k, row, bar);
+  }
+}
+// `rows` <= 128 rows of B from `row`.  K-major: one box for 128 rows (a box of 32 at a time cost
+// 10% there), else as many low ones as the tile needs.  MN-major as A; blocks start at multiples
+// of 64 only where tiles do, so a narrow tile's blocks come one by one from the flat map.
+constexpr int kLowBox = 32;
+template <int MN>
+__device__ __forceinline__ uint32_t b_bytes(int rows) {
+  const int box = MN ? 64 : kLowBox;
+  return (uint32_t)((rows + box - 1) / box * box * kBK * 2);
+}
+template <int MN>
+__device__ __forceinline__ void load_b(const PairMaps& m, const CUtensorMap* map,
+                                       const CUtensorMap* low, void* s, int row, int rows, int k,
+                                       uint64_t* bar) {
+  unsigned char* d = static_cast<unsigned char*>(s);
+  if (rows == kPairHalf && (!MN || m.b3)) {
+    if (MN)
+      pair_load_3d(s, map, 0, k, row >> 6, bar);
+    else
+      pair_load_2d(s, map, k, row, bar);
+    return;
+  }
+  constexpr int box = MN ? 64 : kLowBox;
+  for (int r = 0; r < rows; r += box, d += box * kBK * 2) {
+    if (MN)
+      pair_load_2d(d, low, row + r, k, bar);
+    else
+      pair_load_2d(d, low, k, row + r, bar);
   }
 }
 
 struct NoEarly {};
+
+// 32 bytes of global memory that nothing else reads, one whole sector (ALIGNED32), or as two
+// 16-byte loads.
+__device__ __forceinline__ void load32(const uint4* p, bool aligned32, uint4& a, uint4& b) {
+  if (aligned32) {
+    asm volatile(
+        "ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+        : "l"(p));
+  } else {
+    a = __ldg(p);
+    b = __ldg(p + 1);
+  }
+}
 
 // ------------------------------------------------------------------ gate
 template <int ACT, bool KEEP, bool CKPT8>
@@ -104,8 +159,9 @@ struct GateProb {
   static constexpr int kAMN = 0, kBMN = 0;
   struct Params {
     int* status;
+    PairWalk walk;  // a tile of width w holds w / 2 columns of g and the same of u
     int64_t N, runs;
-    int f, m_tiles, n_tiles, nk;
+    int f, nk;
     int8_t *cg, *cu;
     float *sg, *su;
   };
@@ -114,17 +170,19 @@ struct GateProb {
   };
   using Early = NoEarly;
   __device__ static void prefetch(const Params&, const Tile&, const PairEpi&, Early&) {}
-  __device__ static int num_tiles(const Params& P) { return P.m_tiles * P.n_tiles; }
+  __device__ static int num_tiles(const Params& P) { return P.walk.total; }
   __device__ static int num_kblocks(const Params& P) { return P.nk; }
   __device__ static Tile tile(const Params& P, int u) {
-    int mt, nt;
-    band_tile(u, P.m_tiles, P.n_tiles, &mt, &nt);
-    return Tile{mt * kPairM, nt * kPairHalf, 256};
+    const WalkTile t = walk_tile(P.walk, u);
+    return Tile{t.mt * kPairM, t.n0 / 2, t.w};
+  }
+  __device__ static uint32_t load_bytes(const PairMaps&, const Tile& t) {
+    return kPairStage / 2 + b_bytes<0>(t.w / 2);
   }
   __device__ static void load(const Params&, const PairMaps& m, const Tile& t, int kb, int rank,
                               void* sa, void* sb, uint64_t* bar) {
-    load_half<0>(&m.a0, sa, t.m0 + rank * kPairHalf, kb * kBK, bar);
-    load_half<0>(rank ? &m.b1 : &m.b0, sb, t.f0, kb * kBK, bar);
+    load_a<0>(m, &m.a0, sa, t.m0 + rank * kPairHalf, kb * kBK, bar);
+    load_b<0>(m, rank ? &m.b1 : &m.b0, rank ? &m.low1 : &m.low0, sb, t.f0, t.w / 2, kb * kBK, bar);
   }
   __device__ static void keep8(const Params& P, const uint32_t (&r)[32], int64_t run_idx,
                                int8_t* codes, float* scale) {
@@ -142,28 +200,28 @@ struct GateProb {
     d[1] = make_uint4(w[4], w[5], w[6], w[7]);
     scale[run_idx] = s.scale;
   }
-  __device__ static void epilogue(const Params& P, const Tile& t, const PairEpi& e, const Early&) {
+  __device__ static void epilogue(const Params& P, const Tile& t, PairEpi& e, const Early&) {
     const int y0 = t.m0 + e.row0;
     const int64_t row = (int64_t)y0 + e.lane;
     if (y0 >= P.N) return;  // warp-uniform
-    for (int piece = e.set; piece < 4; piece += 2) {
+    for (int piece = e.set; piece * 64 < t.w; piece += 2) {
       const int c0 = t.f0 + piece * 32;
       if (c0 >= P.f) break;  // warp-uniform
       uint32_t g[32], u[32], p[16];
       tmem_ld32(e.taddr + piece * 32, g);
-      tmem_ld32(e.taddr + kPairHalf + piece * 32, u);
+      tmem_ld32(e.taddr + t.w / 2 + piece * 32, u);
       tmem_wait_ld(g);
       tmem_wait_ld(u);
-      staging_free(e.lane);
+      unsigned char* stg = staging_next(e);
       if (KEEP && !CKPT8) {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           p[j] = pack_bf16(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
-        stage_bf16(e.stg + 2048, e.lane, p);
+        stage_bf16(stg + 2048, e.lane, p);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           p[j] = pack_bf16(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
-        stage_bf16(e.stg + 4096, e.lane, p);
+        stage_bf16(stg + 4096, e.lane, p);
       }
       if (KEEP && CKPT8 && row < P.N) {
         const int64_t run = row * P.runs + (c0 >> 5);
@@ -175,13 +233,13 @@ struct GateProb {
         p[j] = pack_bf16(
             act_fast<ACT>(__uint_as_float(g[2 * j])) * __uint_as_float(u[2 * j]),
             act_fast<ACT>(__uint_as_float(g[2 * j + 1])) * __uint_as_float(u[2 * j + 1]));
-      stage_bf16(e.stg, e.lane, p);
+      stage_bf16(stg, e.lane, p);
       staging_ready();
       if (e.lane == 0) {
-        tma_store_2d(&e.maps->o0, e.stg, c0, y0);
+        tma_store_2d(&e.maps->o0, stg, c0, y0);
         if (KEEP && !CKPT8) {
-          tma_store_2d(&e.maps->o1, e.stg + 2048, c0, y0);
-          tma_store_2d(&e.maps->o2, e.stg + 4096, c0, y0);
+          tma_store_2d(&e.maps->o1, stg + 2048, c0, y0);
+          tma_store_2d(&e.maps->o2, stg + 4096, c0, y0);
         }
         bulk_commit();
       }
@@ -196,8 +254,10 @@ struct GateGradProb {
   static constexpr int kAMN = 0, kBMN = 1;
   struct Params {
     int* status;
+    PairWalk walk;
     int64_t N, runs;
-    int f, m_tiles, n_tiles, nk, w;
+    int f, nk;
+    bool aligned32;     // rows of g and u start on 32-byte boundaries
     const void *g, *u;  // bf16 values or int8 codes
     const float *sg, *su;
   };
@@ -208,37 +268,46 @@ struct GateGradProb {
     uint4 g[CKPT8 ? 2 : 4], u[CKPT8 ? 2 : 4];
     float sg, su;
   };
-  __device__ static int num_tiles(const Params& P) { return P.m_tiles * P.n_tiles; }
+  __device__ static int num_tiles(const Params& P) { return P.walk.total; }
   __device__ static int num_kblocks(const Params& P) { return P.nk; }
   __device__ static Tile tile(const Params& P, int u) {
-    int mt, nt;
-    band_tile(u, P.m_tiles, P.n_tiles, &mt, &nt);
-    return Tile{mt * kPairM, nt * P.w, P.w};
+    const WalkTile t = walk_tile(P.walk, u);
+    return Tile{t.mt * kPairM, t.n0, t.w};
+  }
+  __device__ static uint32_t load_bytes(const PairMaps&, const Tile& t) {
+    return kPairStage / 2 + b_bytes<1>(t.w / 2);
   }
   __device__ static void load(const Params&, const PairMaps& m, const Tile& t, int kb, int rank,
                               void* sa, void* sb, uint64_t* bar) {
-    load_half<0>(&m.a0, sa, t.m0 + rank * kPairHalf, kb * kBK, bar);
-    load_half<1>(&m.b0, sb, t.n0 + rank * (t.w / 2), kb * kBK, bar);
+    load_a<0>(m, &m.a0, sa, t.m0 + rank * kPairHalf, kb * kBK, bar);
+    load_b<1>(m, &m.b0, &m.low0, sb, t.n0 + rank * (t.w / 2), t.w / 2, kb * kBK, bar);
   }
   __device__ static void fetch(const Params& P, int64_t row, int c0, Early& k) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
     const bool in = row < P.N && c0 < P.f;
+    const uint4 *g = static_cast<const uint4*>(P.g), *u = static_cast<const uint4*>(P.u);
     if (CKPT8) {
       const int64_t run = in ? row * P.runs + (c0 >> 5) : 0;
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        k.g[v] = in ? __ldg(static_cast<const uint4*>(P.g) + run * 2 + v) : zero;
-        k.u[v] = in ? __ldg(static_cast<const uint4*>(P.u) + run * 2 + v) : zero;
+      k.g[0] = k.g[1] = k.u[0] = k.u[1] = zero;
+      k.sg = k.su = 0.f;
+      if (in) {
+        load32(g + run * 2, P.aligned32, k.g[0], k.g[1]);
+        load32(u + run * 2, P.aligned32, k.u[0], k.u[1]);
+        k.sg = __ldg(P.sg + run);
+        k.su = __ldg(P.su + run);
       }
-      k.sg = in ? __ldg(P.sg + run) : 0.f;
-      k.su = in ? __ldg(P.su + run) : 0.f;
     } else {
       const int64_t at = in ? (row * P.f + c0) >> 3 : 0;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const bool has = in && c0 + 8 * v < P.f;
-        k.g[v] = has ? __ldg(static_cast<const uint4*>(P.g) + at + v) : zero;
-        k.u[v] = has ? __ldg(static_cast<const uint4*>(P.u) + at + v) : zero;
+      for (int v = 0; v < 4; v += 2) {
+        k.g[v] = k.g[v + 1] = k.u[v] = k.u[v + 1] = zero;
+        if (in && c0 + 8 * v + 8 < P.f) {
+          load32(g + at + v, P.aligned32, k.g[v], k.g[v + 1]);
+          load32(u + at + v, P.aligned32, k.u[v], k.u[v + 1]);
+        } else if (in && c0 + 8 * v < P.f) {  // the row ends after 8 columns
+          k.g[v] = __ldg(g + at + v);
+          k.u[v] = __ldg(u + at + v);
+        }
       }
     }
   }
@@ -260,7 +329,7 @@ struct GateGradProb {
       }
     }
   }
-  __device__ static void epilogue(const Params& P, const Tile& t, const PairEpi& e, Early& k) {
+  __device__ static void epilogue(const Params& P, const Tile& t, PairEpi& e, Early& k) {
     const int y0 = t.m0 + e.row0;
     const int64_t row = (int64_t)y0 + e.lane;
     if (y0 >= P.N) return;  // warp-uniform
@@ -293,15 +362,15 @@ struct GateGradProb {
           pu[2 * j + i] = pack_bf16(du[2 * i], du[2 * i + 1]);
         }
       }
-      staging_free(e.lane);
-      stage_bf16(e.stg, e.lane, ph);
-      stage_bf16(e.stg + 2048, e.lane, pg);
-      stage_bf16(e.stg + 4096, e.lane, pu);
+      unsigned char* stg = staging_next(e);
+      stage_bf16(stg, e.lane, ph);
+      stage_bf16(stg + 2048, e.lane, pg);
+      stage_bf16(stg + 4096, e.lane, pu);
       staging_ready();
       if (e.lane == 0) {
-        tma_store_2d(&e.maps->o0, e.stg, c0, y0);
-        tma_store_2d(&e.maps->o1, e.stg + 2048, c0, y0);
-        tma_store_2d(&e.maps->o2, e.stg + 4096, c0, y0);
+        tma_store_2d(&e.maps->o0, stg, c0, y0);
+        tma_store_2d(&e.maps->o1, stg + 2048, c0, y0);
+        tma_store_2d(&e.maps->o2, stg + 4096, c0, y0);
         bulk_commit();
       }
     }
@@ -310,37 +379,41 @@ struct GateGradProb {
 
 // ------------------------------------------------------------------ plain products
 // out[rows x cols] = A B^T.  A second product may follow the first in the same accumulator
-// (k-blocks from nk0 on read a1 and b1), or stand beside it as further tiles (kinds == 2: the
-// second half of the tiles read a1 and write o1).  ADD: fp32 output, +=; else bf16, overwritten.
-template <int AMN, int BMN, bool ADD>
+// (k-blocks from nk0 on read a1 and b1), or stand beside it as further row tiles (those from
+// m_each on read a1 and write o1).  ADD: fp32 output, +=; else bf16, overwritten.  TRANS: the
+// output is stored transposed, out[cols][rows].
+template <int AMN, int BMN, bool ADD, bool TRANS>
 struct PlainProb {
   static constexpr int kAMN = AMN, kBMN = BMN;
   struct Params {
     int* status;
+    PairWalk walk;
     int64_t rows;
-    int cols, m_tiles, n_tiles, kinds, nk, nk0, w;
+    int cols, m_each, nk, nk0;
   };
   struct Tile {
     int m0, n0, w, kind;
   };
   using Early = NoEarly;
   __device__ static void prefetch(const Params&, const Tile&, const PairEpi&, Early&) {}
-  __device__ static int num_tiles(const Params& P) { return P.m_tiles * P.n_tiles * P.kinds; }
+  __device__ static int num_tiles(const Params& P) { return P.walk.total; }
   __device__ static int num_kblocks(const Params& P) { return P.nk; }
   __device__ static Tile tile(const Params& P, int u) {
-    int mt, nt;
-    const int each = P.m_tiles * P.n_tiles;
-    band_tile(u % each, P.m_tiles, P.n_tiles, &mt, &nt);
-    return Tile{mt * kPairM, nt * P.w, P.w, u / each};
+    const WalkTile t = walk_tile(P.walk, u);
+    const int kind = t.mt >= P.m_each;
+    return Tile{(t.mt - kind * P.m_each) * kPairM, t.n0, t.w, kind};
+  }
+  __device__ static uint32_t load_bytes(const PairMaps&, const Tile& t) {
+    return kPairStage / 2 + b_bytes<BMN>(t.w / 2);
   }
   __device__ static void load(const Params& P, const PairMaps& m, const Tile& t, int kb, int rank,
                               void* sa, void* sb, uint64_t* bar) {
     const bool second = kb >= P.nk0;
     const int k = (second ? kb - P.nk0 : kb) * kBK;
-    load_half<AMN>(second || t.kind ? &m.a1 : &m.a0, sa, t.m0 + rank * kPairHalf, k, bar);
-    load_half<BMN>(second ? &m.b1 : &m.b0, sb, t.n0 + rank * (t.w / 2), k, bar);
+    load_a<AMN>(m, second || t.kind ? &m.a1 : &m.a0, sa, t.m0 + rank * kPairHalf, k, bar);
+    load_b<BMN>(m, second ? &m.b1 : &m.b0, second ? &m.low1 : &m.low0, sb, t.n0 + rank * (t.w / 2), t.w / 2, k, bar);
   }
-  __device__ static void epilogue(const Params& P, const Tile& t, const PairEpi& e, const Early&) {
+  __device__ static void epilogue(const Params& P, const Tile& t, PairEpi& e, const Early&) {
     const int y0 = t.m0 + e.row0;
     if (y0 >= P.rows) return;  // warp-uniform
     const CUtensorMap* out = t.kind ? &e.maps->o1 : &e.maps->o0;
@@ -350,19 +423,22 @@ struct PlainProb {
       uint32_t r[32];
       tmem_ld32(e.taddr + piece * 32, r);
       tmem_wait_ld(r);
-      staging_free(e.lane);
-      if (ADD) {
-        stage_f32(e.stg, e.lane, r);
+      unsigned char* stg = staging_next(e);
+      if (TRANS) {
+        stage_transposed<ADD>(stg, e.lane, r);
+      } else if (ADD) {
+        stage_f32(stg, e.lane, r);
       } else {
         uint32_t p[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           p[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-        stage_bf16(e.stg, e.lane, p);
+        stage_bf16(stg, e.lane, p);
       }
       staging_ready();
       if (e.lane == 0) {
-        if (ADD) tma_add_2d(out, e.stg, c0, y0); else tma_store_2d(out, e.stg, c0, y0);
+        const int x = TRANS ? y0 : c0, y = TRANS ? c0 : y0;
+        if (ADD) tma_add_2d(out, stg, x, y); else tma_store_2d(out, stg, x, y);
         bulk_commit();
       }
     }
@@ -388,13 +464,31 @@ cudaError_t launch_pair(const FfnPlan& p, const PairMaps& maps, const typename P
   return cudaGetLastError();
 }
 
-// [rows][cols] bf16 as an operand whose K runs along the row (boxes of 64 k x 128 rows) or
-// down the rows (64 columns x 64 k).
-bool map_kmajor(CUtensorMap* m, const void* base, int64_t rows, int cols) {
-  return make_tmap_bf16_2d(m, base, cols, rows, (uint64_t)cols * 2, kBK, kPairHalf);
+// [rows][cols] bf16 as an operand whose K runs along the row ...
+bool map_kmajor(CUtensorMap* m, const void* base, int64_t rows, int cols, int box) {
+  return make_tmap_bf16_2d(m, base, cols, rows, (uint64_t)cols * 2, kBK, box);
 }
+// ... or down the rows: flat (64 columns x 64 k), or in blocks of 64 columns, two to a load.
 bool map_mnmajor(CUtensorMap* m, const void* base, int64_t rows, int cols) {
   return make_tmap_bf16_2d(m, base, cols, rows, (uint64_t)cols * 2, 64, kBK);
+}
+bool map_blocks(CUtensorMap* m, const void* base, int64_t rows, int cols) {
+  const uint64_t dims[3] = {64, (uint64_t)rows, (uint64_t)cols / 64};
+  const uint64_t strides[2] = {(uint64_t)cols * 2, 128};
+  const uint32_t box[3] = {64, kBK, 2};
+  return make_tmap_store(m, false, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool map_a_mn(PairMaps* m, CUtensorMap* a, const void* base, int64_t rows, int cols) {
+  m->a3 = cols % 64 == 0;
+  return m->a3 ? map_blocks(a, base, rows, cols) : map_mnmajor(a, base, rows, cols);
+}
+bool map_b_mn(PairMaps* m, CUtensorMap* b, CUtensorMap* low, const void* base, int64_t rows,
+              int cols) {
+  m->b3 = cols % 64 == 0;
+  return map_mnmajor(low, base, rows, cols) && (!m->b3 || map_blocks(b, base, rows, cols));
+}
+bool map_b_k(CUtensorMap* b, CUtensorMap* low, const void* base, int64_t rows, int cols) {
+  return map_kmajor(b, base, rows, cols, kPairHalf) && map_kmajor(low, base, rows, cols, kLowBox);
 }
 bool map_out(CUtensorMap* m, bool fp32, void* base, int64_t rows, int cols) {
   const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
@@ -406,16 +500,59 @@ bool map_out(CUtensorMap* m, bool fp32, void* base, int64_t rows, int cols) {
 
 int64_t tiles_of(int64_t rows, int w) { return (rows + w - 1) / w; }
 
-// Output-tile width: the multiple of 32 whose rounds over the SM pairs times width is least;
-// ties go to the wider tile, which reads fewer operand bytes per product.
-int pair_width(int64_t m_tiles, int cols, int pairs) {
-  int best = 256;
-  int64_t cost = -1;
-  for (int w = 256; w >= 128; w -= 32) {
-    const int64_t c = tiles_of(m_tiles * tiles_of(cols, w), pairs) * w;
-    if (cost < 0 || c < cost) {
-      cost = c;
-      best = w;
+// Time of a tile of width w in units of the products of one column: the products themselves, or
+// the operand bytes of a k-block (A's 128 rows and B's w / 2 per CTA at the rate at which 128
+// rows of B would just keep up), whichever is longer.
+int tile_cost(int w) { return std::max(w, 128 + w / 2); }
+
+// The rounds that are left after the whole ones: n1 tiles of cost c1, then n2 of cost c2, as
+// tile_of_round deals them out.  The longest share is that of the first or the last pair or of one
+// beside the place where the tiles change or end.
+int64_t tail_cost(int64_t n1, int c1, int64_t n2, int c2, int pairs) {
+  const int64_t n = n1 + n2;
+  const auto share = [&](int64_t p) {
+    int64_t sum = 0;
+    for (int64_t r = 0; r * pairs < n; ++r) {
+      const int64_t u = r * pairs + (r & 1 ? pairs - 1 - p : p);
+      if (u < n) sum += u < n1 ? c1 : c2;
+    }
+    return sum;
+  };
+  int64_t most = std::max(share(0), share(pairs - 1));
+  for (const int64_t end : {n1, n})
+    for (int64_t u = std::max<int64_t>(end - 1, 0); u <= end; ++u) {
+      const int64_t i = u % pairs;
+      most = std::max(most, std::max(share(i), share(pairs - 1 - i)));
+    }
+  return most;
+}
+
+// The walk of least cost over tile widths and cuts of the remaining wide tiles.  Widths below
+// 192 lose more to operand bytes than they gain in balance; a cut leaves pieces of 32 columns
+// at least (step: 64 for the gate, whose halves are pieces of their own).
+PairWalk make_walk(int64_t m_tiles, int64_t cols, int pairs, int step) {
+  PairWalk best{};
+  int64_t least = -1;
+  for (int w = 256; w >= 192; w -= 32) {
+    if (w % step) continue;
+    PairWalk k{};
+    k.m_tiles = (int)m_tiles;
+    k.width = w;
+    k.full_n = (int)(cols / w);
+    k.rest = (int)((cols % w + step - 1) / step * step);
+    const int64_t wide = m_tiles * k.full_n;
+    k.whole = (int)(wide / pairs * pairs);
+    for (int s = 1; s <= 4; s *= 2) {
+      if (w % (s * step)) continue;
+      k.split = s;
+      const int64_t left = (wide - k.whole) * s, narrow = k.rest ? m_tiles : 0;
+      k.total = (int)(k.whole + left + narrow);
+      const int64_t cost = (int64_t)k.whole / pairs * tile_cost(w) +
+                           tail_cost(left, tile_cost(w / s), narrow, tile_cost(k.rest), pairs);
+      if (least < 0 || cost < least) {
+        least = cost;
+        best = k;
+      }
     }
   }
   return best;
@@ -439,8 +576,7 @@ cudaError_t run_gate(const FfnPlan& p, const PairMaps& m, const pkm_ffn_saved* s
   P.N = p.N;
   P.runs = p.runs;
   P.f = p.d_ff;
-  P.m_tiles = (int)tiles_of(p.N, kPairM);
-  P.n_tiles = (int)tiles_of(p.d_ff, kPairHalf);
+  P.walk = make_walk(tiles_of(p.N, kPairM), 2 * (int64_t)p.d_ff, p.sm_count / 2, 64);
   P.nk = (int)tiles_of(p.d_in, kBK);
   if (KEEP && CKPT8) {
     P.cg = static_cast<int8_t*>(s->g);
@@ -448,7 +584,7 @@ cudaError_t run_gate(const FfnPlan& p, const PairMaps& m, const pkm_ffn_saved* s
     P.sg = s->g_scale;
     P.su = s->u_scale;
   }
-  return launch_pair<G>(p, m, P, (int64_t)P.m_tiles * P.n_tiles, st);
+  return launch_pair<G>(p, m, P, P.walk.total, st);
 }
 
 template <int ACT, bool CKPT8>
@@ -460,33 +596,31 @@ cudaError_t run_gate_grad(const FfnPlan& p, const PairMaps& m, const pkm_ffn_sav
   P.N = p.N;
   P.runs = p.runs;
   P.f = p.d_ff;
-  P.m_tiles = (int)tiles_of(p.N, kPairM);
-  P.w = pair_width(P.m_tiles, p.d_ff, p.sm_count / 2);
-  P.n_tiles = (int)tiles_of(p.d_ff, P.w);
+  P.walk = make_walk(tiles_of(p.N, kPairM), p.d_ff, p.sm_count / 2, 32);
   P.nk = (int)tiles_of(p.d_out, kBK);
   P.g = s.g;
   P.u = s.u;
+  P.aligned32 = (((uintptr_t)s.g | (uintptr_t)s.u) & 31) == 0 && (CKPT8 || p.d_ff % 16 == 0);
   P.sg = s.g_scale;
   P.su = s.u_scale;
-  return launch_pair<G>(p, m, P, (int64_t)P.m_tiles * P.n_tiles, st);
+  return launch_pair<G>(p, m, P, P.walk.total, st);
 }
 
-// out (+)= A B^T with k of length K (or K0 then K more).
-template <int AMN, int BMN, bool ADD>
+// out (+)= A B^T over k of length K, once or with a second pair of operands after the first, for
+// one or two kinds of row tiles.
+template <int AMN, int BMN, bool ADD, bool TRANS>
 cudaError_t run_plain(const FfnPlan& p, const PairMaps& m, int64_t rows, int cols, int64_t K,
                       int kinds, bool twice, cudaStream_t st) {
-  using G = PlainProb<AMN, BMN, ADD>;
+  using G = PlainProb<AMN, BMN, ADD, TRANS>;
   typename G::Params P{};
   P.status = p.status;
   P.rows = rows;
   P.cols = cols;
-  P.kinds = kinds;
-  P.m_tiles = (int)tiles_of(rows, kPairM);
-  P.w = pair_width((int64_t)P.m_tiles * kinds, cols, p.sm_count / 2);
-  P.n_tiles = (int)tiles_of(cols, P.w);
+  P.m_each = (int)tiles_of(rows, kPairM);
+  P.walk = make_walk((int64_t)P.m_each * kinds, cols, p.sm_count / 2, 32);
   P.nk0 = (int)tiles_of(K, kBK);
   P.nk = twice ? 2 * P.nk0 : P.nk0;
-  return launch_pair<G>(p, m, P, (int64_t)P.m_tiles * P.n_tiles * kinds, st);
+  return launch_pair<G>(p, m, P, P.walk.total, st);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -502,9 +636,9 @@ cudaError_t launch_ffn_fwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
                               const void* Wd, void* y, const pkm_ffn_saved* s, void* ws,
                               cudaStream_t st) {
   PairMaps m{};
-  FFN_MAP(map_kmajor(&m.a0, x, p.N, p.d_in));
-  FFN_MAP(map_kmajor(&m.b0, Wg, p.d_ff, p.d_in));
-  FFN_MAP(map_kmajor(&m.b1, Wu, p.d_ff, p.d_in));
+  FFN_MAP(map_kmajor(&m.a0, x, p.N, p.d_in, kPairHalf));
+  FFN_MAP(map_b_k(&m.b0, &m.low0, Wg, p.d_ff, p.d_in));
+  FFN_MAP(map_b_k(&m.b1, &m.low1, Wu, p.d_ff, p.d_in));
   FFN_MAP(map_out(&m.o0, false, ws, p.N, p.d_ff));
   if (s && !p.ckpt8) {
     FFN_MAP(map_out(&m.o1, false, s->g, p.N, p.d_ff));
@@ -517,10 +651,10 @@ cudaError_t launch_ffn_fwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
   if (p.act == PKM_ACT_GELU) FFN_GATE(PKM_ACT_GELU); else FFN_GATE(PKM_ACT_SILU);
 #undef FFN_GATE
   PairMaps d{};
-  FFN_MAP(map_kmajor(&d.a0, ws, p.N, p.d_ff));
-  FFN_MAP(map_kmajor(&d.b0, Wd, p.d_out, p.d_ff));
+  FFN_MAP(map_kmajor(&d.a0, ws, p.N, p.d_ff, kPairHalf));
+  FFN_MAP(map_b_k(&d.b0, &d.low0, Wd, p.d_out, p.d_ff));
   FFN_MAP(map_out(&d.o0, false, y, p.N, p.d_out));
-  return run_plain<0, 0, false>(p, d, p.N, p.d_out, p.d_ff, 1, false, st);
+  return run_plain<0, 0, false, false>(p, d, p.N, p.d_out, p.d_ff, 1, false, st);
 }
 
 cudaError_t launch_ffn_bwd_tc(const FfnPlan& p, const void* x, const void* Wg, const void* Wu,
@@ -532,8 +666,8 @@ cudaError_t launch_ffn_bwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
   char* dg = h + each;
   char* du = dg + each;
   PairMaps m{};
-  FFN_MAP(map_kmajor(&m.a0, dy, p.N, p.d_out));
-  FFN_MAP(map_mnmajor(&m.b0, Wd, p.d_out, p.d_ff));
+  FFN_MAP(map_kmajor(&m.a0, dy, p.N, p.d_out, kPairHalf));
+  FFN_MAP(map_b_mn(&m, &m.b0, &m.low0, Wd, p.d_out, p.d_ff));
   FFN_MAP(map_out(&m.o0, false, h, p.N, p.d_ff));
   FFN_MAP(map_out(&m.o1, false, dg, p.N, p.d_ff));
   FFN_MAP(map_out(&m.o2, false, du, p.N, p.d_ff));
@@ -543,34 +677,34 @@ cudaError_t launch_ffn_bwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
   if (p.act == PKM_ACT_GELU) FFN_GRAD(PKM_ACT_GELU); else FFN_GRAD(PKM_ACT_SILU);
 #undef FFN_GRAD
   const bool add = !p.grad_bf16;
-  if (dWd) {
+  if (dWd) {  // as (h^T dy) stored transposed: h's columns are the ones that fill row tiles
     PairMaps w{};
-    FFN_MAP(map_mnmajor(&w.a0, dy, p.N, p.d_out));
-    FFN_MAP(map_mnmajor(&w.b0, h, p.N, p.d_ff));
+    FFN_MAP(map_a_mn(&w, &w.a0, h, p.N, p.d_ff));
+    FFN_MAP(map_b_mn(&w, &w.b0, &w.low0, dy, p.N, p.d_out));
     FFN_MAP(map_out(&w.o0, add, dWd, p.d_out, p.d_ff));
-    FFN_TRY(add ? run_plain<1, 1, true>(p, w, p.d_out, p.d_ff, p.N, 1, false, st)
-                : run_plain<1, 1, false>(p, w, p.d_out, p.d_ff, p.N, 1, false, st));
+    FFN_TRY(add ? run_plain<1, 1, true, true>(p, w, p.d_ff, p.d_out, p.N, 1, false, st)
+                : run_plain<1, 1, false, true>(p, w, p.d_ff, p.d_out, p.N, 1, false, st));
   }
   if (dWg || dWu) {
     PairMaps w{};
     void* first = dWg ? dWg : dWu;
-    FFN_MAP(map_mnmajor(&w.a0, dWg ? dg : du, p.N, p.d_ff));
-    FFN_MAP(map_mnmajor(&w.a1, du, p.N, p.d_ff));
-    FFN_MAP(map_mnmajor(&w.b0, x, p.N, p.d_in));
+    FFN_MAP(map_a_mn(&w, &w.a0, dWg ? dg : du, p.N, p.d_ff));
+    FFN_MAP(map_a_mn(&w, &w.a1, du, p.N, p.d_ff));
+    FFN_MAP(map_b_mn(&w, &w.b0, &w.low0, x, p.N, p.d_in));
     FFN_MAP(map_out(&w.o0, add, first, p.d_ff, p.d_in));
     if (dWg && dWu) FFN_MAP(map_out(&w.o1, add, dWu, p.d_ff, p.d_in));
     const int kinds = dWg && dWu ? 2 : 1;
-    FFN_TRY(add ? run_plain<1, 1, true>(p, w, p.d_ff, p.d_in, p.N, kinds, false, st)
-                : run_plain<1, 1, false>(p, w, p.d_ff, p.d_in, p.N, kinds, false, st));
+    FFN_TRY(add ? run_plain<1, 1, true, false>(p, w, p.d_ff, p.d_in, p.N, kinds, false, st)
+                : run_plain<1, 1, false, false>(p, w, p.d_ff, p.d_in, p.N, kinds, false, st));
   }
   if (dx) {
     PairMaps w{};
-    FFN_MAP(map_kmajor(&w.a0, dg, p.N, p.d_ff));
-    FFN_MAP(map_kmajor(&w.a1, du, p.N, p.d_ff));
-    FFN_MAP(map_mnmajor(&w.b0, Wg, p.d_ff, p.d_in));
-    FFN_MAP(map_mnmajor(&w.b1, Wu, p.d_ff, p.d_in));
+    FFN_MAP(map_kmajor(&w.a0, dg, p.N, p.d_ff, kPairHalf));
+    FFN_MAP(map_kmajor(&w.a1, du, p.N, p.d_ff, kPairHalf));
+    FFN_MAP(map_b_mn(&w, &w.b0, &w.low0, Wg, p.d_ff, p.d_in));
+    FFN_MAP(map_b_mn(&w, &w.b1, &w.low1, Wu, p.d_ff, p.d_in));
     FFN_MAP(map_out(&w.o0, false, dx, p.N, p.d_in));
-    FFN_TRY((run_plain<0, 1, false>(p, w, p.N, p.d_in, p.d_ff, 1, true, st)));
+    FFN_TRY((run_plain<0, 1, false, false>(p, w, p.N, p.d_in, p.d_ff, 1, true, st)));
   }
   return cudaSuccess;
 }

@@ -30,12 +30,16 @@ constexpr int kPairM = 256;                  // rows of a tile: 128 per CTA
 constexpr int kPairHalf = 128;               // rows of A, and at most of B, per CTA
 constexpr int kPairStage = 2 * kPairHalf * kBK * 2;  // 32 KiB: A half, then B half
 constexpr int kPairThreads = 320;
-constexpr int kPairStages = 5;
-constexpr int kPairStg = 6144;               // staging bytes per epilogue warp
+constexpr int kPairStages = 4;
+constexpr int kPairStg = 2 * 6144;           // staging bytes per epilogue warp: two sets
 constexpr size_t kPairSmem = 1024 + (size_t)kPairStages * kPairStage + 8 * kPairStg;
 
+// Operands and outputs.  A K-major B has a second map with low boxes for narrow tiles.  An
+// MN-major operand whose columns are whole blocks of 64 is mapped as blocks (a3, b3), so that one
+// load brings two of them.
 struct PairMaps {
-  CUtensorMap a0, a1, b0, b1, o0, o1, o2;
+  CUtensorMap a0, a1, b0, b1, low0, low1, o0, o1, o2;
+  bool a3, b3;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -57,6 +61,14 @@ __device__ __forceinline__ void pair_load_2d(void* smem_dst, const CUtensorMap* 
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(smem_dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(even_cta_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void pair_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y,
+                                             int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(even_cta_addr(bar))
       : "memory");
 }
 __device__ __forceinline__ void pair_mma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
@@ -81,11 +93,52 @@ __device__ __forceinline__ void arrive_even_cta(uint64_t* bar) {
                : "memory");
 }
 
+// ------------------------------------------------------------------ the walk over tiles
+// Column tiles of `width` and one narrower for the rest; every pair of CTAs takes one tile of a
+// round.  Wide tiles fill whole rounds first.  What is left then is short: the remaining wide
+// tiles, each cut into `split` column pieces, and after them the narrow ones, which go round in
+// turns of alternating direction, so that a pair with a wide piece is the last to get another.
+constexpr int kBand = 8;
+struct PairWalk {
+  int m_tiles;  // row tiles (all kinds together)
+  int full_n;   // column tiles of full width
+  int width;    // a multiple of 32
+  int rest;     // width of the last column tile, a multiple of 32, or 0
+  int whole;    // wide tiles in whole rounds
+  int split;    // column pieces of each remaining wide tile
+  int total;
+};
+struct WalkTile {
+  int mt, n0, w;
+};
+// Wide tiles go in bands of kBand row tiles, all column tiles of a band before the next, so that
+// the tiles in flight share rows of A and of B in L2.
+__device__ __forceinline__ WalkTile walk_tile(const PairWalk& W, int u) {
+  const int wide = W.m_tiles * W.full_n;
+  int part = 0, i = u, w = W.width;
+  if (u >= W.whole) {
+    const int v = u - W.whole, left = (wide - W.whole) * W.split;
+    if (v >= left) return WalkTile{v - left, W.full_n * W.width, W.rest};
+    i = W.whole + v / W.split;
+    part = v % W.split;
+    w = W.width / W.split;
+  }
+  const int per = kBand * W.full_n, b = i / per, r = i % per;
+  const int rows = min(kBand, W.m_tiles - b * kBand);
+  return WalkTile{b * kBand + r % rows, r / rows * W.width + part * w, w};
+}
+// The tile of CTA pair `pair` in round r.
+__device__ __forceinline__ int tile_of_round(int r, int pair, int pairs, int whole) {
+  const bool back = r * pairs >= whole && ((r - whole / pairs) & 1);
+  return r * pairs + (back ? pairs - 1 - pair : pair);
+}
+
 // What an epilogue call works with: the tile, its accumulator, the warp's place.
 struct PairEpi {
   const PairMaps* maps;
   uint32_t taddr;      // TMEM address of the accumulator's column 0 on this warp's lanes
-  unsigned char* stg;  // the warp's staging bytes (1024-byte aligned)
+  unsigned char* stg;  // the warp's staging bytes (1024-byte aligned), two sets used in turn
+  int turn;            // the set that the next piece uses
   int row0;            // first row of the warp's 32, relative to the tile
   int set;             // 0: even pieces, 1: odd
   int lane;
@@ -96,7 +149,7 @@ struct PairEpi {
 //   Params              with int* status
 //   Tile, tile(P, u)    the u-th tile; Tile::w is its MMA width (a multiple of 32)
 //   num_tiles(P), num_kblocks(P)
-//   load(P, maps, t, kb, rank, sa, sb, bar)   exactly kPairStage bytes
+//   load(P, maps, t, kb, rank, sa, sb, bar)   load_bytes(maps, t) bytes per CTA
 //   epilogue(P, t, epi)
 template <class Prob>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
@@ -113,7 +166,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const int first = (int)(blockIdx.x >> 1), stride = (int)(gridDim.x >> 1);
+  const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -150,15 +203,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int u = first; u < ntiles && ok; u += stride) {
+      for (int r = 0; r * pairs < ntiles && ok; ++r) {
+        const int u = tile_of_round(r, pair, pairs, P.walk.whole);
+        if (u >= ntiles) continue;
         const typename Prob::Tile t = Prob::tile(P, u);
+        const uint32_t bytes = 2 * Prob::load_bytes(maps, t);
         for (int kb = 0; kb < nk; ++kb) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_flag, status)) {
             ok = false;
             break;
           }
           unsigned char* sa = smem + (size_t)stage * kPairStage;
-          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * kPairStage);
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], bytes);
           Prob::load(P, maps, t, kb, (int)rank, sa, sa + kPairStage / 2, &full_bar[stage]);
           if (++stage == S) {
             stage = 0;
@@ -180,7 +236,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true, issued = false;
-      for (int u = first; u < ntiles && ok; u += stride) {
+      for (int r = 0; r * pairs < ntiles && ok; ++r) {
+        const int u = tile_of_round(r, pair, pairs, P.walk.whole);
+        if (u >= ntiles) continue;
         const typename Prob::Tile t = Prob::tile(P, u);
         const uint32_t idesc = idesc_bf16(kPairM, t.w, Prob::kAMN, Prob::kBMN);
         if (!mbar_wait(&tempty_bar[acc], ((acc_phase >> acc) & 1u) ^ 1u, &abort_flag, status))
@@ -219,7 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     // every product, and every arrival its commits send to either CTA, is done before TMEM and
     // shared memory are given up
-    if (lane == 0 && first < ntiles && !abort_flag) {
+    if (lane == 0 && pair < ntiles && !abort_flag) {
       const long long t0 = clock64();
       while (!mbar_try_wait_sleep(&drain_bar, 0, 2000u) && !abort_flag &&
              clock64() - t0 < kWaitBudgetCycles) {
@@ -231,12 +289,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     PairEpi epi;
     epi.maps = &maps;
     epi.stg = smem + (size_t)S * kPairStage + (size_t)(warp - 2) * kPairStg;
+    epi.turn = 0;
     epi.row0 = (int)rank * kPairHalf + quarter * 32;
     epi.set = (warp - 2) >> 2;
     epi.lane = lane;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int u = first; u < ntiles; u += stride) {
+    for (int r = 0; r * pairs < ntiles; ++r) {
+      const int u = tile_of_round(r, pair, pairs, P.walk.whole);
+      if (u >= ntiles) continue;
       const typename Prob::Tile t = Prob::tile(P, u);
       typename Prob::Early early;
       Prob::prefetch(P, t, epi, early);
