@@ -22,19 +22,27 @@ using namespace tc;
 using bf = __nv_bfloat16;
 
 // ------------------------------------------------------------------ device helpers
-// Fast forms: exp and the quotient are good to ~2^-21, far inside the bf16 rounding that
-// every result of them gets.
+// Fast forms: 2^x and the reciprocal are good to ~2^-22, far inside the bf16 rounding that
+// every result of them gets.  (The .ftz forms: the others spend as many instructions again on
+// subnormal operands, which here only arise where the result is 0 or 1 to fp32.)
+__device__ __forceinline__ float sigmoid_fast(float v) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
+}
 template <int ACT>
 __device__ __forceinline__ float act_fast(float v) {
   if (ACT == PKM_ACT_GELU) return act_fn<ACT>(v);
-  return __fdividef(v, 1.f + __expf(-v));
+  return v * sigmoid_fast(v);
 }
+// SiLU's slope s (1 + v (1 - s)) with a = v s: s + (a - a s).
 template <int ACT>
 __device__ __forceinline__ void act_and_slope_fast(float v, float* a, float* slope) {
   if (ACT == PKM_ACT_GELU) return act_and_slope<ACT>(v, a, slope);
-  const float s = __fdividef(1.f, 1.f + __expf(-v));
+  const float s = sigmoid_fast(v);
   *a = v * s;
-  *slope = s * fmaf(v, 1.f - s, 1.f);
+  *slope = s + fmaf(-*a, s, *a);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -42,22 +50,27 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// A warp's 32 x 32 bf16 piece into a 2 KiB staging tile (row = lane, 64-byte swizzle: 16-byte
-// chunk v of row r sits at chunk v ^ ((r >> 1) & 3)).
-__device__ __forceinline__ void stage_bf16(unsigned char* stg, int lane, const uint32_t (&p)[16]) {
-  uint4* s = reinterpret_cast<uint4*>(stg) + lane * 4;
+// Columns [32 half, +32) of a warp's 32 x 64 bf16 piece into a 4 KiB staging tile (row = lane,
+// 128-byte swizzle: 16-byte chunk v of row r sits at chunk v ^ (r & 7)).  Pieces are 64 columns
+// wide so that a store's rows are whole 128-byte lines: with 32 columns the copy engine, which
+// also brings the operands, had twice the rows to write and bounded the kernels of three outputs.
+__device__ __forceinline__ void stage_bf16(unsigned char* stg, int lane, int half,
+                                           const uint32_t (&p)[16]) {
+  uint4* s = reinterpret_cast<uint4*>(stg) + lane * 8;
 #pragma unroll
   for (int v = 0; v < 4; ++v)
-    s[v ^ ((lane >> 1) & 3)] = make_uint4(p[4 * v], p[4 * v + 1], p[4 * v + 2], p[4 * v + 3]);
+    s[(half * 4 + v) ^ (lane & 7)] =
+        make_uint4(p[4 * v], p[4 * v + 1], p[4 * v + 2], p[4 * v + 3]);
 }
+// A warp's 32 x 32 fp32 piece, the same way.
 __device__ __forceinline__ void stage_f32(unsigned char* stg, int lane, const uint32_t (&r)[32]) {
   uint4* s = reinterpret_cast<uint4*>(stg) + lane * 8;
 #pragma unroll
   for (int v = 0; v < 8; ++v)
     s[v ^ (lane & 7)] = make_uint4(r[4 * v], r[4 * v + 1], r[4 * v + 2], r[4 * v + 3]);
 }
-// The piece transposed: its column j becomes row j of the staged tile, 32 lanes side by side (the
-// swizzles of the two above).
+// A 32 x 32 piece transposed: its column j becomes row j of the staged tile, 32 lanes side by
+// side (64-byte swizzle for bf16, 128-byte for fp32).
 template <bool F32>
 __device__ __forceinline__ void stage_transposed(unsigned char* stg, int lane,
                                                  const uint32_t (&r)[32]) {
@@ -79,14 +92,10 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, const void* s
       "r"(smem_u32(src)), "r"(x), "r"(y)
       : "memory");
 }
-// The next set of staging bytes, once the stores of the piece before last have read it (every
-// piece is one group of stores).
-__device__ __forceinline__ unsigned char* staging_next(PairEpi& e) {
-  if (e.lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+// The warp's earlier stores have read its staging bytes.
+__device__ __forceinline__ void staging_free(int lane) {
+  if (lane == 0) bulk_wait_read_all();
   __syncwarp();
-  unsigned char* s = e.stg + e.turn * (kPairStg / 2);
-  e.turn ^= 1;
-  return s;
 }
 __device__ __forceinline__ void staging_ready() {
   fence_proxy_async_smem();
@@ -157,6 +166,7 @@ __device__ __forceinline__ void load32(const uint4* p, bool aligned32, uint4& a,
 template <int ACT, bool KEEP, bool CKPT8>
 struct GateProb {
   static constexpr int kAMN = 0, kBMN = 0;
+  static constexpr int kStg = KEEP && !CKPT8 ? 3 * 4096 : 4096;
   struct Params {
     int* status;
     PairWalk walk;  // a tile of width w holds w / 2 columns of g and the same of u
@@ -200,49 +210,53 @@ struct GateProb {
     d[1] = make_uint4(w[4], w[5], w[6], w[7]);
     scale[run_idx] = s.scale;
   }
-  __device__ static void epilogue(const Params& P, const Tile& t, PairEpi& e, const Early&) {
+  __device__ static void epilogue(const Params& P, const Tile& t, const PairEpi& e, const Early&) {
     const int y0 = t.m0 + e.row0;
     const int64_t row = (int64_t)y0 + e.lane;
     if (y0 >= P.N) return;  // warp-uniform
-    for (int piece = e.set; piece * 64 < t.w; piece += 2) {
-      const int c0 = t.f0 + piece * 32;
+    for (int piece = e.set; piece * 128 < t.w; piece += 2) {
+      const int c0 = t.f0 + piece * 64;
       if (c0 >= P.f) break;  // warp-uniform
-      uint32_t g[32], u[32], p[16];
-      tmem_ld32(e.taddr + piece * 32, g);
-      tmem_ld32(e.taddr + t.w / 2 + piece * 32, u);
-      tmem_wait_ld(g);
-      tmem_wait_ld(u);
-      unsigned char* stg = staging_next(e);
-      if (KEEP && !CKPT8) {
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t g[32], u[32], p[16];
+        tmem_ld32(e.taddr + piece * 64 + half * 32, g);
+        tmem_ld32(e.taddr + t.w / 2 + piece * 64 + half * 32, u);
+        tmem_wait_ld(g);
+        tmem_wait_ld(u);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          p[j] = pack_bf16(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
-        stage_bf16(stg + 2048, e.lane, p);
+          p[j] = pack_bf16(
+              act_fast<ACT>(__uint_as_float(g[2 * j])) * __uint_as_float(u[2 * j]),
+              act_fast<ACT>(__uint_as_float(g[2 * j + 1])) * __uint_as_float(u[2 * j + 1]));
+        if (half == 0) staging_free(e.lane);
+        stage_bf16(e.stg, e.lane, half, p);
+        if (KEEP && !CKPT8) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          p[j] = pack_bf16(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
-        stage_bf16(stg + 4096, e.lane, p);
-      }
-      if (KEEP && CKPT8 && row < P.N) {
-        const int64_t run = row * P.runs + (c0 >> 5);
-        keep8(P, g, run, P.cg, P.sg);
-        keep8(P, u, run, P.cu, P.su);
-      }
+          for (int j = 0; j < 16; ++j)
+            p[j] = pack_bf16(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
+          stage_bf16(e.stg + 4096, e.lane, half, p);
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        p[j] = pack_bf16(
-            act_fast<ACT>(__uint_as_float(g[2 * j])) * __uint_as_float(u[2 * j]),
-            act_fast<ACT>(__uint_as_float(g[2 * j + 1])) * __uint_as_float(u[2 * j + 1]));
-      stage_bf16(stg, e.lane, p);
+          for (int j = 0; j < 16; ++j)
+            p[j] = pack_bf16(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+          stage_bf16(e.stg + 8192, e.lane, half, p);
+        }
+        if (KEEP && CKPT8 && row < P.N && c0 + half * 32 < P.f) {
+          const int64_t run = row * P.runs + (c0 >> 5) + half;
+          keep8(P, g, run, P.cg, P.sg);
+          keep8(P, u, run, P.cu, P.su);
+        }
+      }
       staging_ready();
       if (e.lane == 0) {
-        tma_store_2d(&e.maps->o0, stg, c0, y0);
+        tma_store_2d(&e.maps->o0, e.stg, c0, y0);
         if (KEEP && !CKPT8) {
-          tma_store_2d(&e.maps->o1, stg + 2048, c0, y0);
-          tma_store_2d(&e.maps->o2, stg + 4096, c0, y0);
+          tma_store_2d(&e.maps->o1, e.stg + 4096, c0, y0);
+          tma_store_2d(&e.maps->o2, e.stg + 8192, c0, y0);
         }
         bulk_commit();
       }
+      __syncwarp();
     }
   }
 };
@@ -252,6 +266,7 @@ struct GateProb {
 template <int ACT, bool CKPT8>
 struct GateGradProb {
   static constexpr int kAMN = 0, kBMN = 1;
+  static constexpr int kStg = 3 * 4096;
   struct Params {
     int* status;
     PairWalk walk;
@@ -312,7 +327,7 @@ struct GateGradProb {
     }
   }
   __device__ static void prefetch(const Params& P, const Tile& t, const PairEpi& e, Early& k) {
-    fetch(P, (int64_t)t.m0 + e.row0 + e.lane, t.n0 + e.set * 32, k);
+    fetch(P, (int64_t)t.m0 + e.row0 + e.lane, t.n0 + e.set * 64, k);
   }
   // Columns 4j .. 4j + 3 of the piece.
   __device__ static void four_of(const uint4* q, float scale, int j, float (&v)[4]) {
@@ -329,50 +344,58 @@ struct GateGradProb {
       }
     }
   }
-  __device__ static void epilogue(const Params& P, const Tile& t, PairEpi& e, Early& k) {
+  __device__ static void epilogue(const Params& P, const Tile& t, const PairEpi& e, Early& k) {
     const int y0 = t.m0 + e.row0;
     const int64_t row = (int64_t)y0 + e.lane;
     if (y0 >= P.N) return;  // warp-uniform
-    for (int piece = e.set; piece * 32 < t.w; piece += 2) {
-      const int c0 = t.n0 + piece * 32;
+    for (int piece = e.set; piece * 64 < t.w; piece += 2) {
+      const int c0 = t.n0 + piece * 64;
       if (c0 >= P.f) break;  // warp-uniform
-      uint32_t d[32], ph[16], pg[16], pu[16];
-      tmem_ld32(e.taddr + piece * 32, d);
-      const Early now = k;
-      if ((piece + 2) * 32 < t.w) fetch(P, row, c0 + 64, k);
-      tmem_wait_ld(d);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t d[32], ph[16], pg[16], pu[16];
+        tmem_ld32(e.taddr + piece * 64 + half * 32, d);
+        const Early now = k;
+        // the next half, or the first of the set's next piece
+        if (half == 0)
+          fetch(P, row, c0 + 32, k);
+        else if ((piece + 2) * 64 < t.w)
+          fetch(P, row, c0 + 128, k);
+        tmem_wait_ld(d);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float g[4], u[4], hh[4], dg[4], du[4];
-        four_of(now.g, now.sg, j, g);
-        four_of(now.u, now.su, j, u);
+        for (int j = 0; j < 8; ++j) {
+          float g[4], u[4], hh[4], dg[4], du[4];
+          four_of(now.g, now.sg, j, g);
+          four_of(now.u, now.su, j, u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float dh = __uint_as_float(d[4 * j + i]);
-          float a, slope;
-          act_and_slope_fast<ACT>(g[i], &a, &slope);
-          hh[i] = a * u[i];
-          dg[i] = dh * u[i] * slope;
-          du[i] = dh * a;
+          for (int i = 0; i < 4; ++i) {
+            const float dh = __uint_as_float(d[4 * j + i]);
+            float a, slope;
+            act_and_slope_fast<ACT>(g[i], &a, &slope);
+            hh[i] = a * u[i];
+            dg[i] = dh * u[i] * slope;
+            du[i] = dh * a;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            ph[2 * j + i] = pack_bf16(hh[2 * i], hh[2 * i + 1]);
+            pg[2 * j + i] = pack_bf16(dg[2 * i], dg[2 * i + 1]);
+            pu[2 * j + i] = pack_bf16(du[2 * i], du[2 * i + 1]);
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          ph[2 * j + i] = pack_bf16(hh[2 * i], hh[2 * i + 1]);
-          pg[2 * j + i] = pack_bf16(dg[2 * i], dg[2 * i + 1]);
-          pu[2 * j + i] = pack_bf16(du[2 * i], du[2 * i + 1]);
-        }
+        if (half == 0) staging_free(e.lane);
+        stage_bf16(e.stg, e.lane, half, ph);
+        stage_bf16(e.stg + 4096, e.lane, half, pg);
+        stage_bf16(e.stg + 8192, e.lane, half, pu);
       }
-      unsigned char* stg = staging_next(e);
-      stage_bf16(stg, e.lane, ph);
-      stage_bf16(stg + 2048, e.lane, pg);
-      stage_bf16(stg + 4096, e.lane, pu);
       staging_ready();
       if (e.lane == 0) {
-        tma_store_2d(&e.maps->o0, stg, c0, y0);
-        tma_store_2d(&e.maps->o1, stg + 2048, c0, y0);
-        tma_store_2d(&e.maps->o2, stg + 4096, c0, y0);
+        tma_store_2d(&e.maps->o0, e.stg, c0, y0);
+        tma_store_2d(&e.maps->o1, e.stg + 4096, c0, y0);
+        tma_store_2d(&e.maps->o2, e.stg + 8192, c0, y0);
         bulk_commit();
       }
+      __syncwarp();
     }
   }
 };
@@ -385,6 +408,7 @@ struct GateGradProb {
 template <int AMN, int BMN, bool ADD, bool TRANS>
 struct PlainProb {
   static constexpr int kAMN = AMN, kBMN = BMN;
+  static constexpr int kStg = ADD ? 2 * 4096 : 4096;
   struct Params {
     int* status;
     PairWalk walk;
@@ -413,34 +437,46 @@ struct PlainProb {
     load_a<AMN>(m, second || t.kind ? &m.a1 : &m.a0, sa, t.m0 + rank * kPairHalf, k, bar);
     load_b<BMN>(m, second ? &m.b1 : &m.b0, second ? &m.low1 : &m.low0, sb, t.n0 + rank * (t.w / 2), t.w / 2, k, bar);
   }
-  __device__ static void epilogue(const Params& P, const Tile& t, PairEpi& e, const Early&) {
+  __device__ static void epilogue(const Params& P, const Tile& t, const PairEpi& e, const Early&) {
     const int y0 = t.m0 + e.row0;
     if (y0 >= P.rows) return;  // warp-uniform
     const CUtensorMap* out = t.kind ? &e.maps->o1 : &e.maps->o0;
-    for (int piece = e.set; piece * 32 < t.w; piece += 2) {
-      const int c0 = t.n0 + piece * 32;
+    for (int piece = e.set; piece * 64 < t.w; piece += 2) {
+      const int c0 = t.n0 + piece * 64;
       if (c0 >= P.cols) break;  // warp-uniform
-      uint32_t r[32];
-      tmem_ld32(e.taddr + piece * 32, r);
-      tmem_wait_ld(r);
-      unsigned char* stg = staging_next(e);
-      if (TRANS) {
-        stage_transposed<ADD>(stg, e.lane, r);
-      } else if (ADD) {
-        stage_f32(stg, e.lane, r);
-      } else {
-        uint32_t p[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          p[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-        stage_bf16(stg, e.lane, p);
+      for (int half = 0; half < 2; ++half) {
+        uint32_t r[32];
+        tmem_ld32(e.taddr + piece * 64 + half * 32, r);
+        tmem_wait_ld(r);
+        if (half == 0) staging_free(e.lane);
+        if (TRANS) {
+          stage_transposed<ADD>(e.stg + half * (kStg / 2), e.lane, r);
+        } else if (ADD) {
+          stage_f32(e.stg + half * (kStg / 2), e.lane, r);
+        } else {
+          uint32_t p[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            p[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+          stage_bf16(e.stg, e.lane, half, p);
+        }
       }
       staging_ready();
       if (e.lane == 0) {
-        const int x = TRANS ? y0 : c0, y = TRANS ? c0 : y0;
-        if (ADD) tma_add_2d(out, stg, x, y); else tma_store_2d(out, stg, x, y);
+        // bf16 rows: one store of 64 columns; else two of 32 columns each
+        for (int half = 0; half < (TRANS || ADD ? 2 : 1); ++half) {
+          const int c = c0 + half * 32;
+          if (c >= P.cols) break;
+          const int x = TRANS ? y0 : c, y = TRANS ? c : y0;
+          if (ADD)
+            tma_add_2d(out, e.stg + half * (kStg / 2), x, y);
+          else
+            tma_store_2d(out, e.stg + half * (kStg / 2), x, y);
+        }
         bulk_commit();
       }
+      __syncwarp();
     }
   }
 };
@@ -453,13 +489,13 @@ cudaError_t launch_pair(const FfnPlan& p, const PairMaps& maps, const typename P
   const uint64_t bit = (uint64_t)1 << p.dev;
   if (!(ready.load(std::memory_order_acquire) & bit)) {
     const cudaError_t e = cudaFuncSetAttribute(
-        tc_pair_kernel<Prob>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+        tc_pair_kernel<Prob>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pair_smem<Prob>());
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
   if (tiles <= 0) return cudaSuccess;
   const int pairs = (int)std::min<int64_t>(tiles, p.sm_count / 2);
-  tc_pair_kernel<Prob><<<2 * pairs, kPairThreads, kPairSmem, st>>>(maps, P);
+  tc_pair_kernel<Prob><<<2 * pairs, kPairThreads, pair_smem<Prob>(), st>>>(maps, P);
   PKM_COUNT(1);
   return cudaGetLastError();
 }
@@ -490,12 +526,14 @@ bool map_b_mn(PairMaps* m, CUtensorMap* b, CUtensorMap* low, const void* base, i
 bool map_b_k(CUtensorMap* b, CUtensorMap* low, const void* base, int64_t rows, int cols) {
   return map_kmajor(b, base, rows, cols, kPairHalf) && map_kmajor(low, base, rows, cols, kLowBox);
 }
-bool map_out(CUtensorMap* m, bool fp32, void* base, int64_t rows, int cols) {
+// An output in boxes of 32 rows x `wide` columns (32 fp32, 64 bf16, or 32 bf16 transposed).
+bool map_out(CUtensorMap* m, bool fp32, void* base, int64_t rows, int cols, uint32_t wide) {
   const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
   const uint64_t strides[1] = {(uint64_t)cols * (fp32 ? 4 : 2)};
-  const uint32_t box[2] = {32, 32};
+  const uint32_t box[2] = {wide, 32};
   return make_tmap_store(m, fp32, 2, base, dims, strides, box,
-                         fp32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+                         wide * (fp32 ? 4 : 2) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                      : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 int64_t tiles_of(int64_t rows, int w) { return (rows + w - 1) / w; }
@@ -528,12 +566,12 @@ int64_t tail_cost(int64_t n1, int c1, int64_t n2, int c2, int pairs) {
 }
 
 // The walk of least cost over tile widths and cuts of the remaining wide tiles.  Widths below
-// 192 lose more to operand bytes than they gain in balance; a cut leaves pieces of 32 columns
-// at least (step: 64 for the gate, whose halves are pieces of their own).
+// 192 lose more to operand bytes than they gain in balance; every width is a multiple of the
+// epilogue's pieces (step: 64, for the gate 128, 64 of each projection).
 PairWalk make_walk(int64_t m_tiles, int64_t cols, int pairs, int step) {
   PairWalk best{};
   int64_t least = -1;
-  for (int w = 256; w >= 192; w -= 32) {
+  for (int w = 256; w >= 192; w -= 64) {
     if (w % step) continue;
     PairWalk k{};
     k.m_tiles = (int)m_tiles;
@@ -576,7 +614,7 @@ cudaError_t run_gate(const FfnPlan& p, const PairMaps& m, const pkm_ffn_saved* s
   P.N = p.N;
   P.runs = p.runs;
   P.f = p.d_ff;
-  P.walk = make_walk(tiles_of(p.N, kPairM), 2 * (int64_t)p.d_ff, p.sm_count / 2, 64);
+  P.walk = make_walk(tiles_of(p.N, kPairM), 2 * (int64_t)p.d_ff, p.sm_count / 2, 128);
   P.nk = (int)tiles_of(p.d_in, kBK);
   if (KEEP && CKPT8) {
     P.cg = static_cast<int8_t*>(s->g);
@@ -596,7 +634,7 @@ cudaError_t run_gate_grad(const FfnPlan& p, const PairMaps& m, const pkm_ffn_sav
   P.N = p.N;
   P.runs = p.runs;
   P.f = p.d_ff;
-  P.walk = make_walk(tiles_of(p.N, kPairM), p.d_ff, p.sm_count / 2, 32);
+  P.walk = make_walk(tiles_of(p.N, kPairM), p.d_ff, p.sm_count / 2, 64);
   P.nk = (int)tiles_of(p.d_out, kBK);
   P.g = s.g;
   P.u = s.u;
@@ -617,7 +655,7 @@ cudaError_t run_plain(const FfnPlan& p, const PairMaps& m, int64_t rows, int col
   P.rows = rows;
   P.cols = cols;
   P.m_each = (int)tiles_of(rows, kPairM);
-  P.walk = make_walk((int64_t)P.m_each * kinds, cols, p.sm_count / 2, 32);
+  P.walk = make_walk((int64_t)P.m_each * kinds, cols, p.sm_count / 2, 64);
   P.nk0 = (int)tiles_of(K, kBK);
   P.nk = twice ? 2 * P.nk0 : P.nk0;
   return launch_pair<G>(p, m, P, P.walk.total, st);
@@ -639,10 +677,10 @@ cudaError_t launch_ffn_fwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
   FFN_MAP(map_kmajor(&m.a0, x, p.N, p.d_in, kPairHalf));
   FFN_MAP(map_b_k(&m.b0, &m.low0, Wg, p.d_ff, p.d_in));
   FFN_MAP(map_b_k(&m.b1, &m.low1, Wu, p.d_ff, p.d_in));
-  FFN_MAP(map_out(&m.o0, false, ws, p.N, p.d_ff));
+  FFN_MAP(map_out(&m.o0, false, ws, p.N, p.d_ff, 64));
   if (s && !p.ckpt8) {
-    FFN_MAP(map_out(&m.o1, false, s->g, p.N, p.d_ff));
-    FFN_MAP(map_out(&m.o2, false, s->u, p.N, p.d_ff));
+    FFN_MAP(map_out(&m.o1, false, s->g, p.N, p.d_ff, 64));
+    FFN_MAP(map_out(&m.o2, false, s->u, p.N, p.d_ff, 64));
   }
 #define FFN_GATE(ACT)                                                              \
   FFN_TRY(!s ? run_gate<ACT, false, false>(p, m, s, st)                            \
@@ -653,7 +691,7 @@ cudaError_t launch_ffn_fwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
   PairMaps d{};
   FFN_MAP(map_kmajor(&d.a0, ws, p.N, p.d_ff, kPairHalf));
   FFN_MAP(map_b_k(&d.b0, &d.low0, Wd, p.d_out, p.d_ff));
-  FFN_MAP(map_out(&d.o0, false, y, p.N, p.d_out));
+  FFN_MAP(map_out(&d.o0, false, y, p.N, p.d_out, 64));
   return run_plain<0, 0, false, false>(p, d, p.N, p.d_out, p.d_ff, 1, false, st);
 }
 
@@ -668,9 +706,9 @@ cudaError_t launch_ffn_bwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
   PairMaps m{};
   FFN_MAP(map_kmajor(&m.a0, dy, p.N, p.d_out, kPairHalf));
   FFN_MAP(map_b_mn(&m, &m.b0, &m.low0, Wd, p.d_out, p.d_ff));
-  FFN_MAP(map_out(&m.o0, false, h, p.N, p.d_ff));
-  FFN_MAP(map_out(&m.o1, false, dg, p.N, p.d_ff));
-  FFN_MAP(map_out(&m.o2, false, du, p.N, p.d_ff));
+  FFN_MAP(map_out(&m.o0, false, h, p.N, p.d_ff, 64));
+  FFN_MAP(map_out(&m.o1, false, dg, p.N, p.d_ff, 64));
+  FFN_MAP(map_out(&m.o2, false, du, p.N, p.d_ff, 64));
 #define FFN_GRAD(ACT)                                              \
   FFN_TRY(p.ckpt8 ? run_gate_grad<ACT, true>(p, m, s, st)          \
                   : run_gate_grad<ACT, false>(p, m, s, st))
@@ -681,7 +719,7 @@ cudaError_t launch_ffn_bwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
     PairMaps w{};
     FFN_MAP(map_a_mn(&w, &w.a0, h, p.N, p.d_ff));
     FFN_MAP(map_b_mn(&w, &w.b0, &w.low0, dy, p.N, p.d_out));
-    FFN_MAP(map_out(&w.o0, add, dWd, p.d_out, p.d_ff));
+    FFN_MAP(map_out(&w.o0, add, dWd, p.d_out, p.d_ff, 32));
     FFN_TRY(add ? run_plain<1, 1, true, true>(p, w, p.d_ff, p.d_out, p.N, 1, false, st)
                 : run_plain<1, 1, false, true>(p, w, p.d_ff, p.d_out, p.N, 1, false, st));
   }
@@ -691,8 +729,8 @@ cudaError_t launch_ffn_bwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
     FFN_MAP(map_a_mn(&w, &w.a0, dWg ? dg : du, p.N, p.d_ff));
     FFN_MAP(map_a_mn(&w, &w.a1, du, p.N, p.d_ff));
     FFN_MAP(map_b_mn(&w, &w.b0, &w.low0, x, p.N, p.d_in));
-    FFN_MAP(map_out(&w.o0, add, first, p.d_ff, p.d_in));
-    if (dWg && dWu) FFN_MAP(map_out(&w.o1, add, dWu, p.d_ff, p.d_in));
+    FFN_MAP(map_out(&w.o0, add, first, p.d_ff, p.d_in, add ? 32 : 64));
+    if (dWg && dWu) FFN_MAP(map_out(&w.o1, add, dWu, p.d_ff, p.d_in, add ? 32 : 64));
     const int kinds = dWg && dWu ? 2 : 1;
     FFN_TRY(add ? run_plain<1, 1, true, false>(p, w, p.d_ff, p.d_in, p.N, kinds, false, st)
                 : run_plain<1, 1, false, false>(p, w, p.d_ff, p.d_in, p.N, kinds, false, st));
@@ -703,7 +741,7 @@ cudaError_t launch_ffn_bwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
     FFN_MAP(map_kmajor(&w.a1, du, p.N, p.d_ff, kPairHalf));
     FFN_MAP(map_b_mn(&w, &w.b0, &w.low0, Wg, p.d_ff, p.d_in));
     FFN_MAP(map_b_mn(&w, &w.b1, &w.low1, Wu, p.d_ff, p.d_in));
-    FFN_MAP(map_out(&w.o0, false, dx, p.N, p.d_in));
+    FFN_MAP(map_out(&w.o0, false, dx, p.N, p.d_in, 64));
     FFN_TRY((run_plain<0, 1, false, false>(p, w, p.N, p.d_in, p.d_ff, 1, true, st)));
   }
   return cudaSuccess;

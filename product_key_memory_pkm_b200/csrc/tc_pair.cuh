@@ -12,7 +12,7 @@
 //   warp 1     MMA issuer (even CTA; allocates TMEM in both): commits every stage back to both
 //              producers and every finished tile to both epilogues
 //   warps 2-9  epilogue (both CTAs): warp w reads TMEM lanes [32 (w & 3), +32); warps 2-5 take
-//              the even 32-column pieces of the tile, 6-9 the odd ones.  Two 256-column
+//              the even 64-column pieces of the tile, 6-9 the odd ones.  Two 256-column
 //              accumulators, so a tile's epilogue runs beside the next tile's products.
 //
 // Operand layouts are those of tc_gemm.cuh (128-byte swizzle; K-major rows of 64 k, or MN-major
@@ -30,9 +30,16 @@ constexpr int kPairM = 256;                  // rows of a tile: 128 per CTA
 constexpr int kPairHalf = 128;               // rows of A, and at most of B, per CTA
 constexpr int kPairStage = 2 * kPairHalf * kBK * 2;  // 32 KiB: A half, then B half
 constexpr int kPairThreads = 320;
-constexpr int kPairStages = 4;
-constexpr int kPairStg = 2 * 6144;           // staging bytes per epilogue warp: two sets
-constexpr size_t kPairSmem = 1024 + (size_t)kPairStages * kPairStage + 8 * kPairStg;
+// The shared memory that an epilogue's staging leaves goes into stages of the ring.
+constexpr int kPairSmemMost = 232448 - 1024 - 512;
+template <class Prob>
+constexpr int pair_stages() {
+  return (kPairSmemMost - 8 * Prob::kStg) / kPairStage;
+}
+template <class Prob>
+constexpr size_t pair_smem() {
+  return 1024 + (size_t)pair_stages<Prob>() * kPairStage + 8 * Prob::kStg;
+}
 
 // Operands and outputs.  A K-major B has a second map with low boxes for narrow tiles.  An
 // MN-major operand whose columns are whole blocks of 64 is mapped as blocks (a3, b3), so that one
@@ -102,8 +109,8 @@ constexpr int kBand = 8;
 struct PairWalk {
   int m_tiles;  // row tiles (all kinds together)
   int full_n;   // column tiles of full width
-  int width;    // a multiple of 32
-  int rest;     // width of the last column tile, a multiple of 32, or 0
+  int width;    // a multiple of 64
+  int rest;     // width of the last column tile, a multiple of 64, or 0
   int whole;    // wide tiles in whole rounds
   int split;    // column pieces of each remaining wide tile
   int total;
@@ -137,8 +144,7 @@ __device__ __forceinline__ int tile_of_round(int r, int pair, int pairs, int who
 struct PairEpi {
   const PairMaps* maps;
   uint32_t taddr;      // TMEM address of the accumulator's column 0 on this warp's lanes
-  unsigned char* stg;  // the warp's staging bytes (1024-byte aligned), two sets used in turn
-  int turn;            // the set that the next piece uses
+  unsigned char* stg;  // the warp's staging bytes (1024-byte aligned)
   int row0;            // first row of the warp's 32, relative to the tile
   int set;             // 0: even pieces, 1: odd
   int lane;
@@ -146,15 +152,17 @@ struct PairEpi {
 
 // A problem provides
 //   kAMN, kBMN          operand layouts (0 K-major, 1 MN-major)
+//   kStg                staging bytes of an epilogue warp (a multiple of 1024)
 //   Params              with int* status
-//   Tile, tile(P, u)    the u-th tile; Tile::w is its MMA width (a multiple of 32)
+//   Tile, tile(P, u)    the u-th tile; Tile::w is its MMA width (a multiple of 64)
 //   num_tiles(P), num_kblocks(P)
 //   load(P, maps, t, kb, rank, sa, sb, bar)   load_bytes(maps, t) bytes per CTA
-//   epilogue(P, t, epi)
+//   prefetch(P, t, epi, early)     loads into registers that the epilogue of t begins with
+//   epilogue(P, t, epi, early)
 template <class Prob>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tc_pair_kernel(const __grid_constant__ PairMaps maps, const typename Prob::Params P) {
-  constexpr int S = kPairStages;
+  constexpr int S = pair_stages<Prob>();
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], tfull_bar[2], tempty_bar[2],
       drain_bar;
@@ -288,8 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int quarter = warp & 3;
     PairEpi epi;
     epi.maps = &maps;
-    epi.stg = smem + (size_t)S * kPairStage + (size_t)(warp - 2) * kPairStg;
-    epi.turn = 0;
+    epi.stg = smem + (size_t)S * kPairStage + (size_t)(warp - 2) * Prob::kStg;
     epi.row0 = (int)rank * kPairHalf + quarter * 32;
     epi.set = (warp - 2) >> 2;
     epi.lane = lane;
