@@ -126,15 +126,16 @@ __device__ __forceinline__ uint32_t b_bytes(int rows) {
   return (uint32_t)((rows + box - 1) / box * box * kBK * 2);
 }
 template <int MN>
-__device__ __forceinline__ void load_b(const PairMaps& m, const CUtensorMap* map,
-                                       const CUtensorMap* low, void* s, int row, int rows, int k,
+__device__ __forceinline__ void load_b(const PairMaps& m,
+                                       int which, void* s, int row, int rows, int k,
                                        uint64_t* bar) {
+  const CUtensorMap* low = &m.low[which];
   unsigned char* d = static_cast<unsigned char*>(s);
-  if (rows == kPairHalf && (!MN || m.b3)) {
+  if (rows == kPairHalf && (!MN || m.b3[which])) {
     if (MN)
-      pair_load_3d(s, map, 0, k, row >> 6, bar);
+      pair_load_3d(s, &m.b[which], 0, k, row >> 6, bar);
     else
-      pair_load_2d(s, map, k, row, bar);
+      pair_load_2d(s, &m.b[which], k, row, bar);
     return;
   }
   constexpr int box = MN ? 64 : kLowBox;
@@ -191,8 +192,8 @@ struct GateProb {
   }
   __device__ static void load(const Params&, const PairMaps& m, const Tile& t, int kb, int rank,
                               void* sa, void* sb, uint64_t* bar) {
-    load_a<0>(m, &m.a0, sa, t.m0 + rank * kPairHalf, kb * kBK, bar);
-    load_b<0>(m, rank ? &m.b1 : &m.b0, rank ? &m.low1 : &m.low0, sb, t.f0, t.w / 2, kb * kBK, bar);
+    load_a<0>(m, &m.a[0], sa, t.m0 + rank * kPairHalf, kb * kBK, bar);
+    load_b<0>(m, rank, sb, t.f0, t.w / 2, kb * kBK, bar);
   }
   __device__ static void keep8(const Params& P, const uint32_t (&r)[32], int64_t run_idx,
                                int8_t* codes, float* scale) {
@@ -249,10 +250,10 @@ struct GateProb {
       }
       staging_ready();
       if (e.lane == 0) {
-        tma_store_2d(&e.maps->o0, e.stg, c0, y0);
+        tma_store_2d(&e.maps->o[0], e.stg, c0, y0);
         if (KEEP && !CKPT8) {
-          tma_store_2d(&e.maps->o1, e.stg + 4096, c0, y0);
-          tma_store_2d(&e.maps->o2, e.stg + 8192, c0, y0);
+          tma_store_2d(&e.maps->o[1], e.stg + 4096, c0, y0);
+          tma_store_2d(&e.maps->o[2], e.stg + 8192, c0, y0);
         }
         bulk_commit();
       }
@@ -294,8 +295,8 @@ struct GateGradProb {
   }
   __device__ static void load(const Params&, const PairMaps& m, const Tile& t, int kb, int rank,
                               void* sa, void* sb, uint64_t* bar) {
-    load_a<0>(m, &m.a0, sa, t.m0 + rank * kPairHalf, kb * kBK, bar);
-    load_b<1>(m, &m.b0, &m.low0, sb, t.n0 + rank * (t.w / 2), t.w / 2, kb * kBK, bar);
+    load_a<0>(m, &m.a[0], sa, t.m0 + rank * kPairHalf, kb * kBK, bar);
+    load_b<1>(m, 0, sb, t.n0 + rank * (t.w / 2), t.w / 2, kb * kBK, bar);
   }
   __device__ static void fetch(const Params& P, int64_t row, int c0, Early& k) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -390,9 +391,9 @@ struct GateGradProb {
       }
       staging_ready();
       if (e.lane == 0) {
-        tma_store_2d(&e.maps->o0, e.stg, c0, y0);
-        tma_store_2d(&e.maps->o1, e.stg + 4096, c0, y0);
-        tma_store_2d(&e.maps->o2, e.stg + 8192, c0, y0);
+        tma_store_2d(&e.maps->o[0], e.stg, c0, y0);
+        tma_store_2d(&e.maps->o[1], e.stg + 4096, c0, y0);
+        tma_store_2d(&e.maps->o[2], e.stg + 8192, c0, y0);
         bulk_commit();
       }
       __syncwarp();
@@ -401,14 +402,54 @@ struct GateGradProb {
 };
 
 // ------------------------------------------------------------------ plain products
-// out[rows x cols] = A B^T.  A second product may follow the first in the same accumulator
-// (k-blocks from nk0 on read a1 and b1), or stand beside it as further row tiles (those from
-// m_each on read a1 and write o1).  ADD: fp32 output, +=; else bf16, overwritten.  TRANS: the
-// output is stored transposed, out[cols][rows].
-template <int AMN, int BMN, bool ADD, bool TRANS>
-struct PlainProb {
-  static constexpr int kAMN = AMN, kBMN = BMN;
-  static constexpr int kStg = ADD ? 2 * 4096 : 4096;
+// A warp's 32 x 64 accumulator columns to the output: bf16 rows in one store, fp32 (ADD: +=) or
+// a transposed piece in two of 32 columns.
+template <bool ADD>
+__device__ __forceinline__ void write_piece(const CUtensorMap* out, const PairEpi& e,
+                                            uint32_t taddr, bool trans, int c0, int y0, int cols) {
+  constexpr int kHalf = ADD ? 4096 : 2048;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t r[32];
+    tmem_ld32(taddr + half * 32, r);
+    tmem_wait_ld(r);
+    if (half == 0) staging_free(e.lane);
+    if (trans) {
+      stage_transposed<ADD>(e.stg + half * kHalf, e.lane, r);
+    } else if (ADD) {
+      stage_f32(e.stg + half * kHalf, e.lane, r);
+    } else {
+      uint32_t p[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        p[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+      stage_bf16(e.stg, e.lane, half, p);
+    }
+  }
+  staging_ready();
+  if (e.lane == 0) {
+    for (int half = 0; half < (trans || ADD ? 2 : 1); ++half) {
+      const int c = c0 + half * 32;
+      if (c >= cols) break;
+      const int x = trans ? y0 : c, y = trans ? c : y0;
+      if (ADD)
+        tma_add_2d(out, e.stg + half * kHalf, x, y);
+      else
+        tma_store_2d(out, e.stg + half * kHalf, x, y);
+    }
+    bulk_commit();
+  }
+  __syncwarp();
+}
+
+// Token rows: out[rows x cols] = A[0] B[0]^T, and for k-blocks from nk0 on A[1] B[1]^T into the
+// same accumulator (y, dx).  SPLIT: so few tiles that k is cut into parts, which are row tiles of
+// their own (part i: k-blocks [i * nk, +nk), past the end zeros) and write fp32 partial
+// results [part][rows][cols]; sum_parts_kernel adds them in order.
+template <int BMN, bool SPLIT>
+struct RowsProb {
+  static constexpr int kAMN = 0, kBMN = BMN;
+  static constexpr int kStg = SPLIT ? 2 * 4096 : 4096;
   struct Params {
     int* status;
     PairWalk walk;
@@ -416,7 +457,7 @@ struct PlainProb {
     int cols, m_each, nk, nk0;
   };
   struct Tile {
-    int m0, n0, w, kind;
+    int m0, n0, w, part;
   };
   using Early = NoEarly;
   __device__ static void prefetch(const Params&, const Tile&, const PairEpi&, Early&) {}
@@ -424,59 +465,109 @@ struct PlainProb {
   __device__ static int num_kblocks(const Params& P) { return P.nk; }
   __device__ static Tile tile(const Params& P, int u) {
     const WalkTile t = walk_tile(P.walk, u);
-    const int kind = t.mt >= P.m_each;
-    return Tile{(t.mt - kind * P.m_each) * kPairM, t.n0, t.w, kind};
+    const int part = SPLIT ? t.mt / P.m_each : 0;
+    return Tile{(t.mt - part * P.m_each) * kPairM, t.n0, t.w, part};
   }
   __device__ static uint32_t load_bytes(const PairMaps&, const Tile& t) {
     return kPairStage / 2 + b_bytes<BMN>(t.w / 2);
   }
   __device__ static void load(const Params& P, const PairMaps& m, const Tile& t, int kb, int rank,
                               void* sa, void* sb, uint64_t* bar) {
-    const bool second = kb >= P.nk0;
+    if (SPLIT) kb += t.part * P.nk;
+    const int second = kb >= P.nk0;
     const int k = (second ? kb - P.nk0 : kb) * kBK;
-    load_a<AMN>(m, second || t.kind ? &m.a1 : &m.a0, sa, t.m0 + rank * kPairHalf, k, bar);
-    load_b<BMN>(m, second ? &m.b1 : &m.b0, second ? &m.low1 : &m.low0, sb, t.n0 + rank * (t.w / 2), t.w / 2, k, bar);
+    load_a<0>(m, &m.a[second], sa, t.m0 + rank * kPairHalf, k, bar);
+    load_b<BMN>(m, second, sb, t.n0 + rank * (t.w / 2), t.w / 2, k, bar);
   }
   __device__ static void epilogue(const Params& P, const Tile& t, const PairEpi& e, const Early&) {
     const int y0 = t.m0 + e.row0;
     if (y0 >= P.rows) return;  // warp-uniform
-    const CUtensorMap* out = t.kind ? &e.maps->o1 : &e.maps->o0;
     for (int piece = e.set; piece * 64 < t.w; piece += 2) {
       const int c0 = t.n0 + piece * 64;
       if (c0 >= P.cols) break;  // warp-uniform
+      if (!SPLIT) {
+        write_piece<false>(&e.maps->o[0], e, e.taddr + piece * 64, false, c0, y0, P.cols);
+        continue;
+      }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t r[32];
         tmem_ld32(e.taddr + piece * 64 + half * 32, r);
         tmem_wait_ld(r);
         if (half == 0) staging_free(e.lane);
-        if (TRANS) {
-          stage_transposed<ADD>(e.stg + half * (kStg / 2), e.lane, r);
-        } else if (ADD) {
-          stage_f32(e.stg + half * (kStg / 2), e.lane, r);
-        } else {
-          uint32_t p[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            p[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-          stage_bf16(e.stg, e.lane, half, p);
-        }
+        stage_f32(e.stg + half * 4096, e.lane, r);
       }
       staging_ready();
       if (e.lane == 0) {
-        // bf16 rows: one store of 64 columns; else two of 32 columns each
-        for (int half = 0; half < (TRANS || ADD ? 2 : 1); ++half) {
-          const int c = c0 + half * 32;
-          if (c >= P.cols) break;
-          const int x = TRANS ? y0 : c, y = TRANS ? c : y0;
-          if (ADD)
-            tma_add_2d(out, e.stg + half * (kStg / 2), x, y);
-          else
-            tma_store_2d(out, e.stg + half * (kStg / 2), x, y);
-        }
+        for (int half = 0; half < 2 && c0 + half * 32 < P.cols; ++half)
+          tma_store_3d(&e.maps->o[0], e.stg + half * 4096, c0 + half * 32, y0, t.part);
         bulk_commit();
       }
       __syncwarp();
+    }
+  }
+};
+
+// out = sum of the parts in order, rounded to bf16.  A thread has 8 columns.
+__global__ void __launch_bounds__(256) sum_parts_kernel(int64_t chunks, int64_t part_stride,
+                                                        int parts, const float* src, bf* dst) {
+  grid_dependency_wait();
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= chunks) return;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < parts; ++p) {
+    const float4* s = reinterpret_cast<const float4*>(src + p * part_stride + i * 8);
+    const float4 a = s[0], b = s[1];
+    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  }
+  reinterpret_cast<uint4*>(dst)[i] =
+      make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                 pack_bf16(v[6], v[7]));
+}
+
+// Weight gradients: D[d_ff rows x cols] = A^T B over the tokens, up to three kinds of row tiles:
+// dg^T x (dWg), du^T x (dWu) and h^T dy, which is stored transposed (dWd [d_out][d_ff]): d_ff is
+// what fills row tiles in all of them.  One launch for all of a width, so their last tiles share
+// a round.  ADD: fp32, +=; else bf16, overwritten.
+template <bool ADD>
+struct WeightProb {
+  static constexpr int kAMN = 1, kBMN = 1;
+  static constexpr int kStg = ADD ? 2 * 4096 : 4096;
+  struct Params {
+    int* status;
+    PairWalk walk;
+    int rows, cols, m_each, nk;
+    int which[3];  // of the kinds present, in order: 0 dWg, 1 dWu, 2 dWd
+  };
+  struct Tile {
+    int m0, n0, w, which;
+  };
+  using Early = NoEarly;
+  __device__ static void prefetch(const Params&, const Tile&, const PairEpi&, Early&) {}
+  __device__ static int num_tiles(const Params& P) { return P.walk.total; }
+  __device__ static int num_kblocks(const Params& P) { return P.nk; }
+  __device__ static Tile tile(const Params& P, int u) {
+    const WalkTile t = walk_tile(P.walk, u);
+    const int kind = t.mt / P.m_each;
+    return Tile{(t.mt - kind * P.m_each) * kPairM, t.n0, t.w,
+                kind == 0 ? P.which[0] : kind == 1 ? P.which[1] : P.which[2]};
+  }
+  __device__ static uint32_t load_bytes(const PairMaps&, const Tile& t) {
+    return kPairStage / 2 + b_bytes<1>(t.w / 2);
+  }
+  __device__ static void load(const Params&, const PairMaps& m, const Tile& t, int kb, int rank,
+                              void* sa, void* sb, uint64_t* bar) {
+    load_a<1>(m, &m.a[t.which], sa, t.m0 + rank * kPairHalf, kb * kBK, bar);
+    load_b<1>(m, t.which == 2, sb, t.n0 + rank * (t.w / 2), t.w / 2, kb * kBK, bar);
+  }
+  __device__ static void epilogue(const Params& P, const Tile& t, const PairEpi& e, const Early&) {
+    const int y0 = t.m0 + e.row0;
+    if (y0 >= P.rows) return;  // warp-uniform
+    for (int piece = e.set; piece * 64 < t.w; piece += 2) {
+      const int c0 = t.n0 + piece * 64;
+      if (c0 >= P.cols) break;  // warp-uniform
+      write_piece<ADD>(&e.maps->o[t.which], e, e.taddr + piece * 64, t.which == 2, c0, y0, P.cols);
     }
   }
 };
@@ -514,17 +605,18 @@ bool map_blocks(CUtensorMap* m, const void* base, int64_t rows, int cols) {
   const uint32_t box[3] = {64, kBK, 2};
   return make_tmap_store(m, false, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-bool map_a_mn(PairMaps* m, CUtensorMap* a, const void* base, int64_t rows, int cols) {
+bool map_a_mn(PairMaps* m, int i, const void* base, int64_t rows, int cols) {
   m->a3 = cols % 64 == 0;
-  return m->a3 ? map_blocks(a, base, rows, cols) : map_mnmajor(a, base, rows, cols);
+  return m->a3 ? map_blocks(&m->a[i], base, rows, cols) : map_mnmajor(&m->a[i], base, rows, cols);
 }
-bool map_b_mn(PairMaps* m, CUtensorMap* b, CUtensorMap* low, const void* base, int64_t rows,
-              int cols) {
-  m->b3 = cols % 64 == 0;
-  return map_mnmajor(low, base, rows, cols) && (!m->b3 || map_blocks(b, base, rows, cols));
+bool map_b_mn(PairMaps* m, int i, const void* base, int64_t rows, int cols) {
+  m->b3[i] = cols % 64 == 0;
+  return map_mnmajor(&m->low[i], base, rows, cols) &&
+         (!m->b3[i] || map_blocks(&m->b[i], base, rows, cols));
 }
-bool map_b_k(CUtensorMap* b, CUtensorMap* low, const void* base, int64_t rows, int cols) {
-  return map_kmajor(b, base, rows, cols, kPairHalf) && map_kmajor(low, base, rows, cols, kLowBox);
+bool map_b_k(PairMaps* m, int i, const void* base, int64_t rows, int cols) {
+  return map_kmajor(&m->b[i], base, rows, cols, kPairHalf) &&
+         map_kmajor(&m->low[i], base, rows, cols, kLowBox);
 }
 // An output in boxes of 32 rows x `wide` columns (32 fp32, 64 bf16, or 32 bf16 transposed).
 bool map_out(CUtensorMap* m, bool fp32, void* base, int64_t rows, int cols, uint32_t wide) {
@@ -644,43 +736,98 @@ cudaError_t run_gate_grad(const FfnPlan& p, const PairMaps& m, const pkm_ffn_sav
   return launch_pair<G>(p, m, P, P.walk.total, st);
 }
 
-// out (+)= A B^T over k of length K, once or with a second pair of operands after the first, for
-// one or two kinds of row tiles.
-template <int AMN, int BMN, bool ADD, bool TRANS>
-cudaError_t run_plain(const FfnPlan& p, const PairMaps& m, int64_t rows, int cols, int64_t K,
-                      int kinds, bool twice, cudaStream_t st) {
-  using G = PlainProb<AMN, BMN, ADD, TRANS>;
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Parts of k for a product of few tiles: as many as leave a pair of SMs to each and 16 k-blocks
+// to every part.  (Planned for 74 pairs wherever it runs, so that the workspace depends on the
+// sizes alone.)  One token row tile of 1600 columns with k = 12800: 64 us in one part, 13 in 8.
+int parts_of(int64_t rows, int cols, int64_t nk) {
+  constexpr int kPairs = 74, kMostParts = 8;
+  const int64_t tiles = tiles_of(rows, kPairM) * tiles_of(cols, 256);
+  if (2 * tiles > kPairs || nk < 32) return 1;
+  return (int)std::min<int64_t>({kMostParts, kPairs / tiles, nk / 16});
+}
+size_t part_bytes(int64_t rows, int cols, int64_t nk) {
+  const int parts = parts_of(rows, cols, nk);
+  return parts > 1 ? align256((size_t)parts * rows * cols * 4) : 0;
+}
+
+// out [p.N][cols] bf16 over k of length K, once or with a second pair of operands after the
+// first.  scratch: part_bytes.
+template <int BMN>
+cudaError_t run_rows(const FfnPlan& p, PairMaps& m, void* out, int cols, int64_t K, bool twice,
+                     void* scratch, cudaStream_t st) {
+  const int64_t nk0 = tiles_of(K, kBK), nk = twice ? 2 * nk0 : nk0;
+  const int parts = parts_of(p.N, cols, nk);
+  const int m_each = (int)tiles_of(p.N, kPairM);
+  const auto fill = [&](auto& P) {
+    P.status = p.status;
+    P.rows = p.N;
+    P.cols = cols;
+    P.m_each = m_each;
+    P.walk = make_walk((int64_t)m_each * parts, cols, p.sm_count / 2, 64);
+    P.nk0 = twice ? (int)nk0 : INT32_MAX;  // without a second pair nothing may read its maps
+    P.nk = (int)tiles_of(nk, parts);
+  };
+  if (parts == 1) {
+    using G = RowsProb<BMN, false>;
+    typename G::Params P{};
+    fill(P);
+    FFN_MAP(map_out(&m.o[0], false, out, p.N, cols, 64));
+    return launch_pair<G>(p, m, P, P.walk.total, st);
+  }
+  using G = RowsProb<BMN, true>;
+  typename G::Params P{};
+  fill(P);
+  const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)p.N, (uint64_t)parts};
+  const uint64_t strides[2] = {(uint64_t)cols * 4, (uint64_t)cols * p.N * 4};
+  const uint32_t box[3] = {32, 32, 1};
+  FFN_MAP(make_tmap_store(&m.o[0], true, 3, scratch, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B));
+  FFN_TRY(launch_pair<G>(p, m, P, P.walk.total, st));
+  const int64_t chunks = p.N * cols / 8;
+  const cudaError_t e = launch_dependent(
+      sum_parts_kernel, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, st, chunks,
+      p.N * cols, parts, static_cast<const float*>(scratch), static_cast<bf*>(out));
+  PKM_COUNT(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// The weight gradients among `kinds` (of which[0 ..]); operands and outputs are mapped.
+template <bool ADD>
+cudaError_t run_weights(const FfnPlan& p, const PairMaps& m, const int* which, int kinds, int cols,
+                        cudaStream_t st) {
+  using G = WeightProb<ADD>;
   typename G::Params P{};
   P.status = p.status;
-  P.rows = rows;
+  P.rows = p.d_ff;
   P.cols = cols;
-  P.m_each = (int)tiles_of(rows, kPairM);
+  P.m_each = (int)tiles_of(p.d_ff, kPairM);
   P.walk = make_walk((int64_t)P.m_each * kinds, cols, p.sm_count / 2, 64);
-  P.nk0 = (int)tiles_of(K, kBK);
-  P.nk = twice ? 2 * P.nk0 : P.nk0;
+  P.nk = (int)tiles_of(p.N, kBK);
+  for (int i = 0; i < kinds; ++i) P.which[i] = which[i];
   return launch_pair<G>(p, m, P, P.walk.total, st);
 }
 
-size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-
 }  // namespace
 
-// Forward: h.  Backward: h, dg, du.  All [N][d_ff] bf16.
+// Forward: h.  Backward: h, dg, du.  All [N][d_ff] bf16; then the parts of y or dx.
 size_t ffn_tc_workspace(const FfnPlan& p, bool backward) {
-  return align256((size_t)p.N * p.d_ff * 2) * (backward ? 3 : 1);
+  const size_t each = align256((size_t)p.N * p.d_ff * 2);
+  const int64_t nk = tiles_of(p.d_ff, kBK);
+  return backward ? 3 * each + part_bytes(p.N, p.d_in, 2 * nk) : each + part_bytes(p.N, p.d_out, nk);
 }
 
 cudaError_t launch_ffn_fwd_tc(const FfnPlan& p, const void* x, const void* Wg, const void* Wu,
                               const void* Wd, void* y, const pkm_ffn_saved* s, void* ws,
                               cudaStream_t st) {
   PairMaps m{};
-  FFN_MAP(map_kmajor(&m.a0, x, p.N, p.d_in, kPairHalf));
-  FFN_MAP(map_b_k(&m.b0, &m.low0, Wg, p.d_ff, p.d_in));
-  FFN_MAP(map_b_k(&m.b1, &m.low1, Wu, p.d_ff, p.d_in));
-  FFN_MAP(map_out(&m.o0, false, ws, p.N, p.d_ff, 64));
+  FFN_MAP(map_kmajor(&m.a[0], x, p.N, p.d_in, kPairHalf));
+  FFN_MAP(map_b_k(&m, 0, Wg, p.d_ff, p.d_in));
+  FFN_MAP(map_b_k(&m, 1, Wu, p.d_ff, p.d_in));
+  FFN_MAP(map_out(&m.o[0], false, ws, p.N, p.d_ff, 64));
   if (s && !p.ckpt8) {
-    FFN_MAP(map_out(&m.o1, false, s->g, p.N, p.d_ff, 64));
-    FFN_MAP(map_out(&m.o2, false, s->u, p.N, p.d_ff, 64));
+    FFN_MAP(map_out(&m.o[1], false, s->g, p.N, p.d_ff, 64));
+    FFN_MAP(map_out(&m.o[2], false, s->u, p.N, p.d_ff, 64));
   }
 #define FFN_GATE(ACT)                                                              \
   FFN_TRY(!s ? run_gate<ACT, false, false>(p, m, s, st)                            \
@@ -689,10 +836,10 @@ cudaError_t launch_ffn_fwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
   if (p.act == PKM_ACT_GELU) FFN_GATE(PKM_ACT_GELU); else FFN_GATE(PKM_ACT_SILU);
 #undef FFN_GATE
   PairMaps d{};
-  FFN_MAP(map_kmajor(&d.a0, ws, p.N, p.d_ff, kPairHalf));
-  FFN_MAP(map_b_k(&d.b0, &d.low0, Wd, p.d_out, p.d_ff));
-  FFN_MAP(map_out(&d.o0, false, y, p.N, p.d_out, 64));
-  return run_plain<0, 0, false, false>(p, d, p.N, p.d_out, p.d_ff, 1, false, st);
+  FFN_MAP(map_kmajor(&d.a[0], ws, p.N, p.d_ff, kPairHalf));
+  FFN_MAP(map_b_k(&d, 0, Wd, p.d_out, p.d_ff));
+  char* scratch = static_cast<char*>(ws) + align256((size_t)p.N * p.d_ff * 2);
+  return run_rows<0>(p, d, y, p.d_out, p.d_ff, false, scratch, st);
 }
 
 cudaError_t launch_ffn_bwd_tc(const FfnPlan& p, const void* x, const void* Wg, const void* Wu,
@@ -704,45 +851,52 @@ cudaError_t launch_ffn_bwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
   char* dg = h + each;
   char* du = dg + each;
   PairMaps m{};
-  FFN_MAP(map_kmajor(&m.a0, dy, p.N, p.d_out, kPairHalf));
-  FFN_MAP(map_b_mn(&m, &m.b0, &m.low0, Wd, p.d_out, p.d_ff));
-  FFN_MAP(map_out(&m.o0, false, h, p.N, p.d_ff, 64));
-  FFN_MAP(map_out(&m.o1, false, dg, p.N, p.d_ff, 64));
-  FFN_MAP(map_out(&m.o2, false, du, p.N, p.d_ff, 64));
+  FFN_MAP(map_kmajor(&m.a[0], dy, p.N, p.d_out, kPairHalf));
+  FFN_MAP(map_b_mn(&m, 0, Wd, p.d_out, p.d_ff));
+  FFN_MAP(map_out(&m.o[0], false, h, p.N, p.d_ff, 64));
+  FFN_MAP(map_out(&m.o[1], false, dg, p.N, p.d_ff, 64));
+  FFN_MAP(map_out(&m.o[2], false, du, p.N, p.d_ff, 64));
 #define FFN_GRAD(ACT)                                              \
   FFN_TRY(p.ckpt8 ? run_gate_grad<ACT, true>(p, m, s, st)          \
                   : run_gate_grad<ACT, false>(p, m, s, st))
   if (p.act == PKM_ACT_GELU) FFN_GRAD(PKM_ACT_GELU); else FFN_GRAD(PKM_ACT_SILU);
 #undef FFN_GRAD
-  const bool add = !p.grad_bf16;
-  if (dWd) {  // as (h^T dy) stored transposed: h's columns are the ones that fill row tiles
+  if (dWg || dWu || dWd) {
+    const bool add = !p.grad_bf16;
     PairMaps w{};
-    FFN_MAP(map_a_mn(&w, &w.a0, h, p.N, p.d_ff));
-    FFN_MAP(map_b_mn(&w, &w.b0, &w.low0, dy, p.N, p.d_out));
-    FFN_MAP(map_out(&w.o0, add, dWd, p.d_out, p.d_ff, 32));
-    FFN_TRY(add ? run_plain<1, 1, true, true>(p, w, p.d_ff, p.d_out, p.N, 1, false, st)
-                : run_plain<1, 1, false, true>(p, w, p.d_ff, p.d_out, p.N, 1, false, st));
-  }
-  if (dWg || dWu) {
-    PairMaps w{};
-    void* first = dWg ? dWg : dWu;
-    FFN_MAP(map_a_mn(&w, &w.a0, dWg ? dg : du, p.N, p.d_ff));
-    FFN_MAP(map_a_mn(&w, &w.a1, du, p.N, p.d_ff));
-    FFN_MAP(map_b_mn(&w, &w.b0, &w.low0, x, p.N, p.d_in));
-    FFN_MAP(map_out(&w.o0, add, first, p.d_ff, p.d_in, add ? 32 : 64));
-    if (dWg && dWu) FFN_MAP(map_out(&w.o1, add, dWu, p.d_ff, p.d_in, add ? 32 : 64));
-    const int kinds = dWg && dWu ? 2 : 1;
-    FFN_TRY(add ? run_plain<1, 1, true, false>(p, w, p.d_ff, p.d_in, p.N, kinds, false, st)
-                : run_plain<1, 1, false, false>(p, w, p.d_ff, p.d_in, p.N, kinds, false, st));
+    int which[3], kinds = 0;
+    if (dWg) {
+      FFN_MAP(map_a_mn(&w, 0, dg, p.N, p.d_ff));
+      FFN_MAP(map_out(&w.o[0], add, dWg, p.d_ff, p.d_in, add ? 32 : 64));
+      which[kinds++] = 0;
+    }
+    if (dWu) {
+      FFN_MAP(map_a_mn(&w, 1, du, p.N, p.d_ff));
+      FFN_MAP(map_out(&w.o[1], add, dWu, p.d_ff, p.d_in, add ? 32 : 64));
+      which[kinds++] = 1;
+    }
+    if (kinds) FFN_MAP(map_b_mn(&w, 0, x, p.N, p.d_in));
+    if (dWd) {
+      FFN_MAP(map_a_mn(&w, 2, h, p.N, p.d_ff));
+      FFN_MAP(map_b_mn(&w, 1, dy, p.N, p.d_out));
+      FFN_MAP(map_out(&w.o[2], add, dWd, p.d_out, p.d_ff, 32));
+      which[kinds++] = 2;
+    }
+    const auto run = add ? run_weights<true> : run_weights<false>;
+    if (p.d_in == p.d_out || kinds == 1 || !dWd) {
+      FFN_TRY(run(p, w, which, kinds, dWd ? p.d_out : p.d_in, st));
+    } else {
+      FFN_TRY(run(p, w, which, kinds - 1, p.d_in, st));
+      FFN_TRY(run(p, w, which + kinds - 1, 1, p.d_out, st));
+    }
   }
   if (dx) {
     PairMaps w{};
-    FFN_MAP(map_kmajor(&w.a0, dg, p.N, p.d_ff, kPairHalf));
-    FFN_MAP(map_kmajor(&w.a1, du, p.N, p.d_ff, kPairHalf));
-    FFN_MAP(map_b_mn(&w, &w.b0, &w.low0, Wg, p.d_ff, p.d_in));
-    FFN_MAP(map_b_mn(&w, &w.b1, &w.low1, Wu, p.d_ff, p.d_in));
-    FFN_MAP(map_out(&w.o0, false, dx, p.N, p.d_in, 64));
-    FFN_TRY((run_plain<0, 1, false, false>(p, w, p.N, p.d_in, p.d_ff, 1, true, st)));
+    FFN_MAP(map_kmajor(&w.a[0], dg, p.N, p.d_ff, kPairHalf));
+    FFN_MAP(map_kmajor(&w.a[1], du, p.N, p.d_ff, kPairHalf));
+    FFN_MAP(map_b_mn(&w, 0, Wg, p.d_ff, p.d_in));
+    FFN_MAP(map_b_mn(&w, 1, Wu, p.d_ff, p.d_in));
+    FFN_TRY(run_rows<1>(p, w, dx, p.d_in, p.d_ff, true, du + each, st));
   }
   return cudaSuccess;
 }

@@ -45,8 +45,8 @@ constexpr size_t pair_smem() {
 // MN-major operand whose columns are whole blocks of 64 is mapped as blocks (a3, b3), so that one
 // load brings two of them.
 struct PairMaps {
-  CUtensorMap a0, a1, b0, b1, low0, low1, o0, o1, o2;
-  bool a3, b3;
+  CUtensorMap a[3], b[2], low[2], o[3];
+  bool a3, b3[2];
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
