@@ -106,7 +106,7 @@ struct W4Unit {
   __device__ void load(const Src& S, const W4Shape& sh, int u, int c) {
     // a lane past the row's end reads within the row: its x is zero, and no code is NaN
     const int at = u * (kCols / 2);
-    const uint8_t* p = S.codes + (col(u, c, 0) < sh.d_in ? at : -4 * WORDS * c);
+    const uint8_t* p = S.codes + (u * kCols + 8 * WORDS * c < sh.d_in ? at : -4 * WORDS * c);
     const unsigned short* q = S.scale + sh.group_of(u);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -228,13 +228,10 @@ enum class Few { kF32, kBf16, kGate };  // y fp32, y bf16, or h = act(first) * s
 // Units a warp has in flight, and the CTAs an SM holds: few units and several CTAs, so that
 // the CTAs of one grid are resident together and none waits for another's last loads (one
 // token, 1600 x 6400 x 1600 in bf16: 18 us; two units and 2 CTAs 24, four units and 1 CTA 32).
-#ifndef FEW_B
-#define FEW_B 2
-#define FEW_C 3
-#endif
 template <class Unit, int M, int NT>
-struct Depth {
-  static constexpr int batch = M * NT > 4 ? 1 : (FEW_B * 4 / M / Unit::kWords > 0 ? FEW_B * 4 / M / Unit::kWords : 1), ctas = M * NT > 2 ? 1 : FEW_C;
+struct Depth {  // 4-bit: 8 words per row and matrix in flight, 4 for the two of a gate
+  static constexpr int wide = 8 / M / Unit::kWords;
+  static constexpr int batch = M * NT > 4 || wide < 1 ? 1 : wide, ctas = M * NT > 2 ? 1 : 3;
 };
 template <int M, int NT>
 struct Depth<W16Unit, M, NT> {
@@ -395,12 +392,15 @@ __global__ void __launch_bounds__(kTpb, Depth<Unit, M, NT>::ctas)
 }
 
 // ------------------------------------------------------------------ many rows
-// More than 16 tokens and many output rows: what bounds few_kernel there is not the weights but
-// every 16 rows reading all of x again.  Here a CTA per SM keeps x (or a chunk of its columns)
-// in shared memory, in operand order, and each of its warps takes 32 rows through all of k, so
-// a read of x serves 32 rows.  The number of warps is chosen so that the rows fill whole
-// rounds of the SMs.  Bound by issuing mma.sync with their operands.
-constexpr int kWideRows = 32, kWideWarps = 12, kWideAhead = 1;
+// Many output rows: what bounds few_kernel there is not the weights but every 16 rows reading all
+// of x again, and their sums over warps.  Here a CTA per SM keeps x (or a chunk of its columns) in
+// shared memory and each of its warps takes 16 rows through all of k.  Rows are dealt so that they
+// fill whole rounds of the SMs with as many warps as fit, up to 24: a warp's products depend on
+// one another, and other warps and kWideIlp products at a time fill the gaps.  Against 50264 x
+// 1600: 24 us for 16 tokens (few_kernel 39), 33 for 32 (89), 58 for 64 (140); for 8 tokens both
+// take 20 to 22, so those stay there.  Still bound by the latency of that chain: the weights
+// alone would take 6.6 us, issuing all products about 20.
+constexpr int kWideRows = 16, kWideWarps = 24, kWideIlp = 2;
 constexpr int kWideSmem = 225 * 1024;
 
 // 16 bytes global -> shared without registers; zeros when !has.
@@ -417,40 +417,37 @@ __global__ void __launch_bounds__(32 * kWideWarps, 1)
     wide_kernel(int N, W4Shape sh, int chunk, const bf* __restrict__ x, W4Mat W,
                 float* __restrict__ y) {
   using Unit = W4Unit<WORDS>;
-  constexpr int T = NT * 8;
+  constexpr int T = NT * 8, kIlp = NT < kWideIlp ? NT : kWideIlp;
+  constexpr int kAhead = NT == 8 ? 1 : 2;  // units requested before their use, as registers allow
   extern __shared__ __align__(16) unsigned char xs[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  // the 8 lanes that read 16 bytes at a time are two rows' four columns 16 * WORDS bytes apart:
-  // a pitch of 64, 16, 32 bytes past a multiple of 128 keeps them on different banks for 1 and 2
-  // words, and to two turns for 4
+  // The 8 lanes that read 16 bytes at a time are two rows' four columns 16 * WORDS bytes apart: a
+  // pitch of 64, 16, 32 bytes past a multiple of 128 keeps them on different banks for 1 and 2
+  // words, and to two turns for 4.  (Lanes 2 and 3 taking their 4 words in another order avoids the
+  // second turn and measured the same.)
   const int pitch = chunk * 2 + wide_pad(WORDS);
   const int tiles = (sh.d_out + kWideRows - 1) / kWideRows;
   const int chunks = (sh.d_in + chunk - 1) / chunk;
   for (int first = 0; first < tiles; first += gridDim.x * warps) {  // a round, same for all CTAs
     const int tile = first + warp * gridDim.x + blockIdx.x;
     const bool mine = tile < tiles;
-    const typename Unit::Src s0(W, sh, tile * kWideRows, g, c), s1(W, sh, tile * kWideRows + 16, g, c);
-    float acc[2][NT][4];
+    const typename Unit::Src src(W, sh, tile * kWideRows, g, c);
+    float acc[NT][4];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[r][t][i] = 0.f;
+      for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
     for (int ch = 0; ch < chunks; ++ch) {
       const int k0 = ch * chunk, cols = min(chunk, sh.d_in - k0);
       const int u0 = k0 / Unit::kCols, u1 = u0 + (cols + Unit::kCols - 1) / Unit::kCols;
-      Unit w[kWideAhead][2];  // units u0 .. of both tiles, kWideAhead ahead of their use
+      Unit w[kAhead];  // units u0 .., kAhead ahead of their use
       const auto fetch = [&](int slot, int u) {
-        if (u < u1) {
-          w[slot][0].load(s0, sh, u, c);
-          w[slot][1].load(s1, sh, u, c);
-        }
+        if (u < u1) w[slot].load(src, sh, u, c);
       };
       if (mine) {
 #pragma unroll
-        for (int i = 0; i < kWideAhead; ++i) fetch(i, u0 + i);
+        for (int i = 0; i < kAhead; ++i) fetch(i, u0 + i);
       }
       if (first == 0 || chunks > 1) {
         if (ch > 0 || first > 0) __syncthreads();  // the chunk before has been read
@@ -466,41 +463,45 @@ __global__ void __launch_bounds__(32 * kWideWarps, 1)
       }
       if (!mine) continue;
       const unsigned char* xb = xs + g * pitch;
-      for (int u = u0; u < u1; u += kWideAhead) {
+      for (int u = u0; u < u1; u += kAhead) {
 #pragma unroll
-        for (int i = 0; i < kWideAhead; ++i) {
+        for (int i = 0; i < kAhead; ++i) {
           if (u + i >= u1) break;
-          float p[2][NT][4];
 #pragma unroll
           for (int j = 0; j < WORDS; ++j) {
-            const typename Unit::A a0 = w[i][0].operands(j), a1 = w[i][1].operands(j);
+            const typename Unit::A a = w[i].operands(j);
             const unsigned char* xj = xb + Unit::col(u + i - u0, c, j) * 2;
+            // scaled word by word: no registers for the sums of a whole unit; kIlp products at a
+            // time, since each waits for the one before it
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint4 xv = *reinterpret_cast<const uint4*>(xj + t * 8 * pitch);
-              Unit::mac(p[0][t], a0, xv, j);
-              Unit::mac(p[1][t], a1, xv, j);
+            for (int t = 0; t < NT; t += kIlp) {
+              float p[kIlp][4];
+              uint4 xv[kIlp];
+#pragma unroll
+              for (int e = 0; e < kIlp; ++e)
+                xv[e] = *reinterpret_cast<const uint4*>(xj + (t + e) * 8 * pitch);
+#pragma unroll
+              for (int e = 0; e < kIlp; ++e)
+                mma16816_first(p[e], a.g[0], a.h[0], a.g[1], a.h[1], xv[e].x, xv[e].y);
+#pragma unroll
+              for (int e = 0; e < kIlp; ++e)
+                mma16816(p[e], a.g[2], a.h[2], a.g[3], a.h[3], xv[e].z, xv[e].w);
+#pragma unroll
+              for (int e = 0; e < kIlp; ++e) w[i].close(acc[t + e], p[e]);
             }
           }
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            w[i][0].close(acc[0][t], p[0][t]);
-            w[i][1].close(acc[1][t], p[1][t]);
-          }
-          fetch(i, u + i + kWideAhead);
+          fetch(i, u + i + kAhead);
         }
       }
     }
     if (!mine) continue;
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = t * 8 + 2 * c + (i & 1), o = tile * kWideRows + r * 16 + g + 8 * (i >> 1);
-          if (n < N && o < sh.d_out) y[(int64_t)n * sh.d_out + o] = acc[r][t][i];
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int n = t * 8 + 2 * c + (i & 1), o = tile * kWideRows + g + 8 * (i >> 1);
+        if (n < N && o < sh.d_out) y[(int64_t)n * sh.d_out + o] = acc[t][i];
+      }
   }
 }
 
@@ -530,9 +531,9 @@ cudaError_t launch_wide(int N, const W4Shape& sh, const bf* x, const W4Mat& W, f
   return cudaGetLastError();
 }
 
-// Rows enough that every SM has several warps of 32.
+// Rows enough that every SM has several warps.
 bool wide_form(int64_t N, int d_out, int sm_count) {
-  return N > 16 && d_out >= 4 * kWideRows * sm_count;
+  return N > 8 && d_out >= 4 * kWideRows * sm_count;
 }
 
 // CTAs of a cluster along k: more while the grid leaves SMs empty and every warp still has
@@ -616,6 +617,8 @@ cudaError_t w4(int64_t N, int d_in, int d_out, int group, const bf* x, const W4M
 template <int WORDS>
 cudaError_t wide(int N, const W4Shape& sh, const bf* x, const W4Mat& W, float* y, int sm_count,
                  cudaStream_t st) {
+  if (N <= 8) return launch_wide<WORDS, 1>(N, sh, x, W, y, sm_count, st);
+  if (N <= 16) return launch_wide<WORDS, 2>(N, sh, x, W, y, sm_count, st);
   return N <= 32 ? launch_wide<WORDS, 4>(N, sh, x, W, y, sm_count, st)
                  : launch_wide<WORDS, 8>(N, sh, x, W, y, sm_count, st);
 }

@@ -137,7 +137,10 @@ def random_w4(seed, o, i, group):
                                    # many rows: whole rounds of the SMs and ragged ones, x in
                                    # one piece and in several
                                    (17, 96, 19001), (32, 1600, 40000), (40, 2016, 18944),
-                                   (64, 32, 19999), (64, 4128, 19000), (16, 160, 20000)])
+                                   (64, 32, 19999), (64, 4128, 19000), (16, 160, 20000),
+                                   # large matrices of few tokens, and k in one to eight parts
+                                   (1, 1600, 50264), (9, 2016, 33333), (20, 8192, 700),
+                                   (48, 6400, 1600), (33, 1056, 129), (17, 16384, 64)])
 def test_w4_matvec(n, i, o, group):
     x = rnd(n, n, i).bfloat16()
     codes, scale = random_w4(i, o, i, group)
@@ -168,7 +171,9 @@ def test_w4_matvec_is_reproducible_and_keeps_non_finite_tokens_apart():
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("n,i,f,o,group", [(1, 32, 32, 1, 32), (1, 1600, 6400, 1600, 64),
                                            (3, 96, 160, 50, 64), (8, 1600, 704, 333, 128),
-                                           (17, 416, 512, 668, 32), (64, 640, 1056, 129, 96)])
+                                           (17, 416, 512, 668, 32), (64, 640, 1056, 129, 96),
+                                           (5, 2048, 8192, 2048, 128), (40, 1600, 6400, 1600, 64),
+                                           (64, 96, 20000, 72, 32)])
 def test_w4_block(n, i, f, o, group, act):
     x = rnd(n + i, n, i).bfloat16()
     packed = {k: random_w4(s, a, b, group)
