@@ -134,12 +134,9 @@ struct W4Unit {
     w4_pairs(w[1][j], o.h);
     return o;
   }
-  // t (+)= word j's products with 8 tokens, x their columns; after the last word, acc += scale t
-  __device__ static void mac(float (&t)[4], const A& o, const uint4& x, int j) {
-    if (j == 0)
-      mma16816_first(t, o.g[0], o.h[0], o.g[1], o.h[1], x.x, x.y);
-    else
-      mma16816(t, o.g[0], o.h[0], o.g[1], o.h[1], x.x, x.y);
+  // t = a word's products with 8 tokens, x their columns; then acc += scale * t
+  __device__ static void mac(float (&t)[4], const A& o, const uint4& x) {
+    mma16816_first(t, o.g[0], o.h[0], o.g[1], o.h[1], x.x, x.y);
     mma16816(t, o.g[2], o.h[2], o.g[3], o.h[3], x.z, x.w);
   }
   __device__ void close(float (&acc)[4], const float (&t)[4]) const {
@@ -183,11 +180,8 @@ struct W16Unit {
     uint4 g, h;
   };
   __device__ A operands(int j) const { return A{w[0][j], w[1][j]}; }
-  __device__ static void mac(float (&t)[4], const A& o, const uint4& x, int j) {
-    if (j == 0)
-      mma16816_first(t, o.g.x, o.h.x, o.g.y, o.h.y, x.x, x.y);
-    else
-      mma16816(t, o.g.x, o.h.x, o.g.y, o.h.y, x.x, x.y);
+  __device__ static void mac(float (&t)[4], const A& o, const uint4& x) {
+    mma16816_first(t, o.g.x, o.h.x, o.g.y, o.h.y, x.x, x.y);
     mma16816(t, o.g.z, o.h.z, o.g.w, o.h.w, x.z, x.w);
   }
   __device__ void close(float (&acc)[4], const float (&t)[4]) const {
@@ -231,7 +225,8 @@ enum class Few { kF32, kBf16, kGate };  // y fp32, y bf16, or h = act(first) * s
 template <class Unit, int M, int NT>
 struct Depth {  // 4-bit: 8 words per row and matrix in flight, 4 for the two of a gate
   static constexpr int wide = 8 / M / Unit::kWords;
-  static constexpr int batch = M * NT > 4 || wide < 1 ? 1 : wide, ctas = M * NT > 2 ? 1 : 3;
+  static constexpr int batch = M * NT > 4 || wide < 1 ? 1 : wide;
+  static constexpr int ctas = M * NT <= 2 ? 3 : NT <= 4 ? 2 : 1;
 };
 template <int M, int NT>
 struct Depth<W16Unit, M, NT> {
@@ -292,7 +287,6 @@ __global__ void __launch_bounds__(kTpb, Depth<Unit, M, NT>::ctas)
       for (int b = 0; b < kBatch; ++b) {
         if (u + b * step >= units) break;
         const int v = u + b * step;
-        float t[M][NT][4];
         const auto products = [&](auto edge) {  // edge: the row ends within the unit
 #pragma unroll
           for (int j = 0; j < Unit::kWords; ++j) {
@@ -305,15 +299,15 @@ __global__ void __launch_bounds__(kTpb, Depth<Unit, M, NT>::ctas)
               uint4 xv = make_uint4(0, 0, 0, 0);
               if (!decltype(edge)::value || k < d_in) xv = *reinterpret_cast<const uint4*>(xp[n] + k);
 #pragma unroll
-              for (int m = 0; m < M; ++m) Unit::mac(t[m][n], a[m], xv, j);
+              for (int m = 0; m < M; ++m) {
+                float p[4];  // scaled word by word: the words' chains are independent
+                Unit::mac(p, a[m], xv);
+                w[m][b].close(acc[m][n], p);
+              }
             }
           }
         };
         if ((v + 1) * Unit::kCols > d_in) products(std::true_type{}); else products(std::false_type{});
-#pragma unroll
-        for (int m = 0; m < M; ++m)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) w[m][b].close(acc[m][n], t[m][n]);
       }
       fetch(u + kBatch * step);
     }

@@ -81,8 +81,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 // Columns [32 half, +32) of a warp's 32 x 64 bf16 piece into a 4 KiB staging tile (row = lane,
 // 128-byte swizzle: 16-byte chunk v of row r sits at chunk v ^ (r & 7)).  Pieces are 64 columns
-// wide so that a store's rows are whole 128-byte lines: with 32 columns the copy engine, which
-// also brings the operands, had twice the rows to write and bounded the kernels of three outputs.
+// wide so that a store's rows are whole 128-byte lines and one set of staging tiles is enough,
+// which leaves shared memory for more ring stages (pieces of 32 in two sets measured the same).
 __device__ __forceinline__ void stage_bf16(unsigned char* stg, int lane, int half,
                                            const uint32_t (&p)[16]) {
   uint4* s = reinterpret_cast<uint4*>(stg) + lane * 8;
@@ -769,7 +769,8 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Parts of k for a product of few tiles: as many as leave a pair of SMs to each and 16 k-blocks
 // to every part.  (Planned for 74 pairs wherever it runs, so that the workspace depends on the
-// sizes alone.)  One token row tile of 1600 columns with k = 12800: 64 us in one part, 13 in 8.
+// sizes alone.)  Backward of 64 tokens, 1600 x 6400 x 1600: 66 us, in one part 116; forward 30
+// against 52; of 1024 tokens, 1024 x 4096 x 1024: 72 against 98.
 int parts_of(int64_t rows, int cols, int64_t nk) {
   constexpr int kPairs = 74, kMostParts = 8;
   const int64_t tiles = tiles_of(rows, kPairM) * tiles_of(cols, 256);

@@ -572,8 +572,7 @@ class FfnDims:
 
     def __post_init__(self):
         s = pkm_ffn_dims(self.N, self.d_in, self.d_ff, self.d_out, self.act, self.flags)
-        object.__setattr__(self, "_c", s)
-        object.__setattr__(self, "_ref", ctypes.byref(s))
+        object.__setattr__(self, "_c", s)  # the dims do not change: made once
 
     def c(self) -> pkm_ffn_dims:
         return self._c
@@ -638,7 +637,7 @@ def pkm_ffn_forward(dims: FfnDims, x, Wg, Wu, Wd, y, saved: dict | None = None, 
     o = ck(Wd, "Wd", dt, (d.d_out, d.d_ff))
     s = None if saved is None else ctypes.byref(_ffn_saved_c(ck, d, saved))
     ws, ws_bytes = ck.workspace(workspace, workspace_bytes)
-    _check(load().pkm_ffn_forward(d._ref, xp, g, u, o, yp, s, ws, ws_bytes, ck.stream(stream)),
+    _check(load().pkm_ffn_forward(ctypes.byref(d._c), xp, g, u, o, yp, s, ws, ws_bytes, ck.stream(stream)),
            "pkm_ffn_forward")
 
 
@@ -656,7 +655,7 @@ def pkm_ffn_backward(dims: FfnDims, x, Wg, Wu, Wd, saved: dict, dy, dx=None, dWg
             ck(dWg, "dWg", wt, ins, True), ck(dWu, "dWu", wt, ins, True),
             ck(dWd, "dWd", wt, outs, True))
     ws, ws_bytes = ck.workspace(workspace, workspace_bytes)
-    _check(load().pkm_ffn_backward(d._ref, *args, ws, ws_bytes, ck.stream(stream)),
+    _check(load().pkm_ffn_backward(ctypes.byref(d._c), *args, ws, ws_bytes, ck.stream(stream)),
            "pkm_ffn_backward")
 
 
@@ -762,5 +761,5 @@ def pkm_w4_ffn(dims: FfnDims, x, Wg, Wu, Wd, y, group: int = 64, workspace=None,
     u = _w4(ck, Wu, "Wu", d.d_ff, d.d_in, group)
     o = _w4(ck, Wd, "Wd", d.d_out, d.d_ff, group)
     ws, ws_bytes = ck.workspace(workspace, workspace_bytes)
-    _check(load().pkm_w4_ffn(d._ref, group, xp, ctypes.byref(g), ctypes.byref(u), ctypes.byref(o),
+    _check(load().pkm_w4_ffn(ctypes.byref(d._c), group, xp, ctypes.byref(g), ctypes.byref(u), ctypes.byref(o),
                              yp, ws, ws_bytes, ck.stream(stream)), "pkm_w4_ffn")

@@ -32,6 +32,16 @@ def test_struct_sizes():
     assert ctypes.sizeof(P.pkm_w4) == 2 * ctypes.sizeof(ctypes.c_void_p)
 
 
+def test_dims_can_be_copied_and_pickled():
+    import copy
+    import dataclasses
+    import pickle
+    d = _d(act=P.PKM_ACT_GELU)
+    for e in (copy.deepcopy(d), pickle.loads(pickle.dumps(d))):
+        assert e == d and P.pkm_ffn_saved_bytes(e, "g") == P.pkm_ffn_saved_bytes(d, "g")
+    assert P.pkm_ffn_saved_bytes(dataclasses.replace(d, N=7), "g") == 7 * 136 * 2
+
+
 def test_saved_and_workspace_sizes():
     d = _d()
     assert P.pkm_ffn_saved_bytes(d, "g") == 64 * 136 * 2

@@ -131,6 +131,59 @@ def test_few_tokens(n):
     assert (whole[n:] == 7.0).all()
 
 
+def offset16(t):
+    """The same values at an address that is a multiple of 16 and of no more."""
+    per = 16 // t.element_size()
+    flat = torch.empty(t.numel() + 4 * per, dtype=t.dtype, device="cuda")
+    start = per if flat.data_ptr() % 32 == 0 else 0
+    out = flat[start:start + t.numel()].view(t.shape)
+    assert out.data_ptr() % 32 == 16
+    return out.copy_(t)
+
+
+@pytest.mark.parametrize("n", [5, 300])
+@pytest.mark.parametrize("flags", [0, P.PKM_FFN_CKPT8, P.PKM_F_FP32, P.PKM_F_SIMT])
+def test_tensors_on_16_byte_boundaries(flags, n):
+    """Every tensor at the least alignment the library takes."""
+    di, f, do = 72, 160, 88
+    dtype = torch.float32 if flags & P.PKM_F_FP32 else torch.bfloat16
+    d = P.FfnDims(n, di, f, do, P.PKM_ACT_GELU, flags)
+    t, dy = make(n, di, f, do, dtype, seed=8)
+    t, dy = {k: offset16(v) for k, v in t.items()}, offset16(dy)
+    saved = {k: None if v is None else offset16(v) for k, v in P.alloc_ffn_saved(d).items()}
+    y, rms = offset16(torch.zeros_like(dy)), TWO if dtype == torch.bfloat16 else None
+    P.pkm_ffn_forward(d, **t, y=y, saved=saved, workspace=scratch(d, P.PKM_FWD))
+    check_forward(d, t, "gelu", saved, y, rms)
+    P.pkm_ffn_forward(d, **t, y=y, workspace=scratch(d, P.PKM_FWD))
+    check_forward(d, t, "gelu", None, y, rms)
+    out = {"d" + k: offset16(torch.zeros_like(v, dtype=dtype if k == "x" else torch.float32))
+           for k, v in t.items()}
+    run_backward(d, t, saved, dy, out)
+    check_backward(d, t, "gelu", saved, dy, out, R.roundoff(dtype), rms)
+
+
+# row tiles of 256 and column tiles of 256, 192 and less; k cut into parts (few tiles, long k) and
+# not; weight gradients of one width in one launch or of two widths in two
+@pytest.mark.parametrize("size", [(40, 2048, 2048, 64), (200, 64, 4104, 2048), (513, 1024, 2056, 264),
+                                  (1300, 264, 640, 264), (700, 1608, 1368, 520)])
+def test_tile_walks_and_split_sums(size):
+    n, di, f, do = size
+    d = dims(n, di, f, do, torch.bfloat16, "silu", P.PKM_FFN_GRAD_BF16)
+    t, dy = make(n, di, f, do, torch.bfloat16, seed=n)
+    y, saved = torch.empty(n, do, dtype=torch.bfloat16, device="cuda"), P.alloc_ffn_saved(d)
+    P.pkm_ffn_forward(d, **t, y=y, saved=saved, workspace=scratch(d, P.PKM_FWD))
+    check_forward(d, t, "silu", saved, y, TWO)
+    want = run_backward(d, t, saved, dy, {"d" + k: torch.full_like(t[k], 5.0)
+                                          for k in ("Wg", "Wu", "Wd")})
+    check_backward(d, t, "silu", saved, dy, want, 2.0 ** -8, TWO)
+    for keep in (("dWg",), ("dWu",), ("dWd",), ("dWu", "dWd"), ("dWg", "dWu"), ("dx", "dWd")):
+        out = {k: torch.full_like(want[k], 5.0) for k in keep}
+        P.pkm_ffn_backward(d, **t, saved=saved, dy=dy, workspace=scratch(d, P.PKM_BWD), **out)
+        for k, v in out.items():  # the same sums in the same order, whatever else is asked for
+            assert torch.equal(v, want[k]), (keep, k)
+    assert P.pkm_check_status() == P.PKM_OK
+
+
 @pytest.mark.parametrize("flags", [0, P.PKM_FFN_CKPT8])
 def test_a_training_size(flags):
     """Several tiles in every direction, ragged in all of them."""
