@@ -43,20 +43,31 @@ __device__ __forceinline__ uint32_t mag_bits(float a) { return __float_as_uint(a
 constexpr uint32_t kInfBits = 0x7f800000u;
 
 // The scale of a run whose largest magnitude has the bits `top`, and the factor that takes
-// its values to codes.  top: that magnitude, or -1 for a run with a non-finite value.
+// its values to codes.  top: that magnitude, or -1 for a run with a non-finite value.  The
+// quotient top / 127 comes from the rounded 1 / 127 and one exact remainder, which gives the
+// correctly rounded result for every fp32 mantissa (all 2^23 tried); inv is off by up to 3 of its
+// last places.  Runs outside 1e-30 .. 1e37, where one of the steps could leave the normal
+// numbers, divide.
 struct CkptScale {
   float scale, inv, top;
+  __device__ bool plain() const { return top >= 1e-30f && top <= 1e37f; }
 };
 __device__ __forceinline__ CkptScale ckpt_scale(uint32_t top_bits) {
   CkptScale s;
   s.top = __uint_as_float(top_bits);
-  if (top_bits >= kInfBits) {
-    s.scale = __uint_as_float(0x7fc00000u);
-    s.inv = 0.f;
-    s.top = -1.f;
-  } else {
+  constexpr float k = 1.f / 127.f;
+  const float q = s.top * k;
+  s.scale = fmaf(fmaf(-127.f, q, s.top), k, q);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s.top));
+  s.inv = 127.f * r;
+  if (!s.plain()) {
     s.scale = s.top / 127.f;
-    s.inv = s.top > 0.f ? 127.f / s.top : 0.f;  // overflows to inf below 2^-121: see ckpt_code
+    s.inv = 0.f;
+    if (top_bits >= kInfBits) {
+      s.scale = __uint_as_float(0x7fc00000u);
+      s.top = -1.f;
+    }
   }
   return s;
 }
@@ -67,16 +78,17 @@ __device__ __noinline__ inline int ckpt_code_exact(float a, float top) {
 }
 // Codes of N values, four to a word: 127 a / top rounded to the nearest integer, halves to
 // even.  Adding 1.5 * 2^23 leaves the rounded number in the low bits.  The product a * inv is
-// off by up to 2^-23 of itself, so a quotient that is exactly a half needs care:
+// off by up to 4 of its last places (6e-5 at 127), so a quotient that is exactly a half
+// needs care:
 //   BF16 (values exact in bf16): a quotient 127 a / top that is not a half is at least 2^-16
 //     of it away (254 A 2^z against M (2r + 1) with 8-bit integers A and M), so rounding the
 //     product to 20 significant bits first turns the halves into exact halves and moves no
 //     other across one.  Such halves are frequent there, and this has no branch.
-//   else: where a product lies within 1e-5 of a half, the exact remainder decides.  With
+//   else: where a product lies within 7e-5 of a half, the exact remainder decides.  With
 //     127 a = hi + lo (both fp32) and r the candidate, e = hi - r top is exact (a multiple of
 //     top's last place, below top), so is 2|e| - top, and the sum with 2 lo has the sign of
 //     the exact remainder less a half.
-// A run whose largest magnitude is below 1e-30 (inv may overflow) is formed in 64 bits.
+// Runs that are not plain() are formed in 64 bits.
 template <bool BF16, int N>
 __device__ __forceinline__ void ckpt_codes(const float (&a)[N], const CkptScale& s,
                                            uint32_t (&w)[N / 4]) {
@@ -99,7 +111,7 @@ __device__ __forceinline__ void ckpt_codes(const float (&a)[N], const CkptScale&
     }
     w[j] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   }
-  if (!BF16 && far > 0.5f - 1e-5f) {
+  if (!BF16 && far > 0.5f - 7e-5f) {
 #pragma unroll
     for (int j = 0; j < N / 4; ++j) {
       w[j] = 0;
@@ -115,7 +127,7 @@ __device__ __forceinline__ void ckpt_codes(const float (&a)[N], const CkptScale&
       }
     }
   }
-  if (s.top < 1e-30f && s.top != 0.f) {
+  if (!s.plain() && s.top != 0.f) {
 #pragma unroll
     for (int j = 0; j < N / 4; ++j) {
       w[j] = 0;

@@ -24,6 +24,11 @@ struct Chunk<bf> {
   __device__ void load(const bf* p) { q = __ldcs(reinterpret_cast<const uint4*>(p)); }
   __device__ void zero() { q = make_uint4(0, 0, 0, 0); }
   __device__ void floats(float (&v)[8]) const { bf16x8_to_f32(q, v); }
+  __device__ uint32_t top() const {  // two 16-bit magnitudes at a time
+    constexpr uint32_t m = 0x7fff7fffu;
+    const uint32_t t = __vmaxu2(__vmaxu2(q.x & m, q.y & m), __vmaxu2(q.z & m, q.w & m));
+    return max(t << 16, t & 0xffff0000u);
+  }
   __device__ static void store(bf* p, const float (&v)[8]) {
     uint4 o;
     __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&o);
@@ -43,6 +48,10 @@ struct Chunk<float> {
   __device__ void floats(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  __device__ uint32_t top() const {
+    return max(max(max(mag_bits(a.x), mag_bits(a.y)), max(mag_bits(a.z), mag_bits(a.w))),
+               max(max(mag_bits(b.x), mag_bits(b.y)), max(mag_bits(b.z), mag_bits(b.w))));
   }
   __device__ static void store(float* p, const float (&v)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -78,9 +87,7 @@ __global__ void __launch_bounds__(kTpb) pack_kernel(int64_t chunks, int per_row,
     const int64_t c = base + i * kTpb;
     float v[8];
     in[i].floats(v);
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, mag_bits(v[j]));
+    uint32_t top = in[i].top();
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const CkptScale s = ckpt_scale(top);
