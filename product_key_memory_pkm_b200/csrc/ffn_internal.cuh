@@ -45,22 +45,27 @@ constexpr uint32_t kInfBits = 0x7f800000u;
 // The scale of a run whose largest magnitude has the bits `top`, and the factor that takes
 // its values to codes.  top: that magnitude, or -1 for a run with a non-finite value.  The
 // quotient top / 127 comes from the rounded 1 / 127 and one exact remainder, which gives the
-// correctly rounded result for every fp32 mantissa (all 2^23 tried); inv is off by up to 3 of its
-// last places.  Runs outside 1e-30 .. 1e37, where one of the steps could leave the normal
-// numbers, divide.
+// correctly rounded result for every fp32 mantissa (all 2^23 tried).  inv is correctly rounded or,
+// for values exact in bf16 (BF16), whose codes tolerate it, off by up to 3 of its last places.
+// Runs outside 1e-30 .. 1e37, where one of the steps could leave the normal numbers, divide.
 struct CkptScale {
   float scale, inv, top;
   __device__ bool plain() const { return top >= 1e-30f && top <= 1e37f; }
 };
+template <bool BF16>
 __device__ __forceinline__ CkptScale ckpt_scale(uint32_t top_bits) {
   CkptScale s;
   s.top = __uint_as_float(top_bits);
   constexpr float k = 1.f / 127.f;
   const float q = s.top * k;
   s.scale = fmaf(fmaf(-127.f, q, s.top), k, q);
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s.top));
-  s.inv = 127.f * r;
+  if (BF16) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s.top));
+    s.inv = 127.f * r;
+  } else {
+    s.inv = 127.f / s.top;
+  }
   if (!s.plain()) {
     s.scale = s.top / 127.f;
     s.inv = 0.f;
@@ -77,17 +82,16 @@ __device__ __noinline__ inline int ckpt_code_exact(float a, float top) {
   return top <= 0.f ? 0 : (int)rint((double)a * 127.0 / (double)top);
 }
 // Codes of N values, four to a word: 127 a / top rounded to the nearest integer, halves to
-// even.  Adding 1.5 * 2^23 leaves the rounded number in the low bits.  The product a * inv is
-// off by up to 4 of its last places (6e-5 at 127), so a quotient that is exactly a half
-// needs care:
+// even.  Adding 1.5 * 2^23 leaves the rounded number in the low bits.  The product a * inv is not
+// exact, so a quotient that is a half, or nearly, needs care:
 //   BF16 (values exact in bf16): a quotient 127 a / top that is not a half is at least 2^-16
 //     of it away (254 A 2^z against M (2r + 1) with 8-bit integers A and M), so rounding the
 //     product to 20 significant bits first turns the halves into exact halves and moves no
 //     other across one.  Such halves are frequent there, and this has no branch.
-//   else: where a product lies within 7e-5 of a half, the exact remainder decides.  With
-//     127 a = hi + lo (both fp32) and r the candidate, e = hi - r top is exact (a multiple of
-//     top's last place, below top), so is 2|e| - top, and the sum with 2 lo has the sign of
-//     the exact remainder less a half.
+//   else: the fused product is off by 2^-24 of itself, 7.6e-6 at most; within 1e-5 of a half the
+//     exact remainder decides.  With 127 a = hi + lo (both fp32) and r the candidate, e = hi - r
+//     top is exact (a multiple of top's last place, below top), so is 2|e| - top, and the sum
+//     with 2 lo has the sign of the exact remainder less a half.
 // Runs that are not plain() are formed in 64 bits.
 template <bool BF16, int N>
 __device__ __forceinline__ void ckpt_codes(const float (&a)[N], const CkptScale& s,
@@ -111,7 +115,7 @@ __device__ __forceinline__ void ckpt_codes(const float (&a)[N], const CkptScale&
     }
     w[j] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   }
-  if (!BF16 && far > 0.5f - 7e-5f) {
+  if (!BF16 && far > 0.5f - 1e-5f) {
 #pragma unroll
     for (int j = 0; j < N / 4; ++j) {
       w[j] = 0;

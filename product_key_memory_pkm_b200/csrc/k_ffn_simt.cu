@@ -21,7 +21,7 @@ __device__ __forceinline__ void put(bf* p, float v) { *p = __float2bfloat16_rn(v
 // checkpoint.
 __device__ __forceinline__ void keep8(float v, int64_t run_idx, int lane, int8_t* codes,
                                       float* scale) {
-  const CkptScale s = ckpt_scale(__reduce_max_sync(0xffffffffu, mag_bits(v)));
+  const CkptScale s = ckpt_scale<false>(__reduce_max_sync(0xffffffffu, mag_bits(v)));
   codes[run_idx * kCkptRun + lane] = (int8_t)ckpt_code_exact(v, s.top);
   if (lane == 0) scale[run_idx] = s.scale;
 }
@@ -228,7 +228,7 @@ __device__ __forceinline__ void keep8_of4(const float (&v)[4], bool in, int64_t 
   uint32_t top = max(max(mag_bits(v[0]), mag_bits(v[1])), max(mag_bits(v[2]), mag_bits(v[3])));
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const CkptScale s = ckpt_scale(top);
+  const CkptScale s = ckpt_scale<false>(top);
   uint32_t w[1];
   ckpt_codes<false>(v, s, w);
   if (!in) return;

@@ -229,7 +229,7 @@ struct GateProb {
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < 32; ++j) top = max(top, r[j] & 0x7fffffffu);
-    const CkptScale s = ckpt_scale(top);
+    const CkptScale s = ckpt_scale<false>(top);
     float a[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) a[j] = __uint_as_float(r[j]);
