@@ -80,9 +80,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // Columns [32 half, +32) of a warp's 32 x 64 bf16 piece into a 4 KiB staging tile (row = lane,
-// 128-byte swizzle: 16-byte chunk v of row r sits at chunk v ^ (r & 7)).  Pieces are 64 columns
-// wide so that a store's rows are whole 128-byte lines and one set of staging tiles is enough,
-// which leaves shared memory for more ring stages (pieces of 32 in two sets measured the same).
+// 128-byte swizzle: 16-byte chunk v of row r sits at chunk v ^ (r & 7)), so that a store's rows
+// are whole 128-byte lines.
 __device__ __forceinline__ void stage_bf16(unsigned char* stg, int lane, int half,
                                            const uint32_t (&p)[16]) {
   uint4* s = reinterpret_cast<uint4*>(stg) + lane * 8;
@@ -90,6 +89,15 @@ __device__ __forceinline__ void stage_bf16(unsigned char* stg, int lane, int hal
   for (int v = 0; v < 4; ++v)
     s[(half * 4 + v) ^ (lane & 7)] =
         make_uint4(p[4 * v], p[4 * v + 1], p[4 * v + 2], p[4 * v + 3]);
+}
+// The 32 columns alone, rows of 64 bytes (64-byte swizzle), 2 KiB: for the epilogues of three
+// outputs, where the 48 KiB this saves are a fifth stage of the ring (16384 x 1600 x 6400: gate with
+// kept projections 841 -> 763 thousand cycles, dh 530 -> 493; the waits for operands shrink).
+__device__ __forceinline__ void stage_bf16_32(unsigned char* stg, int lane, const uint32_t (&p)[16]) {
+  uint4* s = reinterpret_cast<uint4*>(stg) + lane * 4;
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    s[v ^ ((lane >> 1) & 3)] = make_uint4(p[4 * v], p[4 * v + 1], p[4 * v + 2], p[4 * v + 3]);
 }
 // A warp's 32 x 32 fp32 piece, the same way.
 __device__ __forceinline__ void stage_f32(unsigned char* stg, int lane, const uint32_t (&r)[32]) {
@@ -178,6 +186,17 @@ __device__ __forceinline__ void load_b(const PairMaps& m,
 
 struct NoEarly {};
 
+// Three staged pieces of 32 columns to the three outputs.
+__device__ __forceinline__ void store3(const PairEpi& e, int c, int y, int cols) {
+  staging_ready();
+  if (e.lane == 0 && c < cols) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) tma_store_2d(&e.maps->o[i], e.stg + 2048 * i, c, y);
+    bulk_commit();
+  }
+  __syncwarp();
+}
+
 // 32 bytes of global memory that nothing else reads, one whole sector (ALIGNED32), or as two
 // 16-byte loads.
 __device__ __forceinline__ void load32(const uint4* p, bool aligned32, uint4& a, uint4& b) {
@@ -196,7 +215,7 @@ __device__ __forceinline__ void load32(const uint4* p, bool aligned32, uint4& a,
 template <int ACT, bool KEEP, bool CKPT8>
 struct GateProb {
   static constexpr int kAMN = 0, kBMN = 0;
-  static constexpr int kStg = KEEP && !CKPT8 ? 3 * 4096 : 4096;
+  static constexpr int kStg = KEEP && !CKPT8 ? 3 * 2048 : 4096;
   struct Params {
     int* status;
     PairWalk walk;  // a tile of width w holds w / 2 columns of g and the same of u
@@ -259,17 +278,21 @@ struct GateProb {
           p[j] = pack_bf16(
               act_fast<ACT>(__uint_as_float(g[2 * j])) * __uint_as_float(u[2 * j]),
               act_fast<ACT>(__uint_as_float(g[2 * j + 1])) * __uint_as_float(u[2 * j + 1]));
-        if (half == 0) staging_free(e.lane);
-        stage_bf16(e.stg, e.lane, half, p);
         if (KEEP && !CKPT8) {
+          staging_free(e.lane);
+          stage_bf16_32(e.stg, e.lane, p);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             p[j] = pack_bf16(__uint_as_float(g[2 * j]), __uint_as_float(g[2 * j + 1]));
-          stage_bf16(e.stg + 4096, e.lane, half, p);
+          stage_bf16_32(e.stg + 2048, e.lane, p);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             p[j] = pack_bf16(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
-          stage_bf16(e.stg + 8192, e.lane, half, p);
+          stage_bf16_32(e.stg + 4096, e.lane, p);
+          store3(e, c0 + half * 32, y0, P.f);
+        } else {
+          if (half == 0) staging_free(e.lane);
+          stage_bf16(e.stg, e.lane, half, p);
         }
         if (KEEP && CKPT8 && row < P.N && c0 + half * 32 < P.f) {
           const int64_t run = row * P.runs + (c0 >> 5) + half;
@@ -277,13 +300,10 @@ struct GateProb {
           keep8(P, u, run, P.cu, P.su);
         }
       }
+      if (KEEP && !CKPT8) continue;
       staging_ready();
       if (e.lane == 0) {
         tma_store_2d(&e.maps->o[0], e.stg, c0, y0);
-        if (KEEP && !CKPT8) {
-          tma_store_2d(&e.maps->o[1], e.stg + 4096, c0, y0);
-          tma_store_2d(&e.maps->o[2], e.stg + 8192, c0, y0);
-        }
         bulk_commit();
       }
       __syncwarp();
@@ -296,7 +316,7 @@ struct GateProb {
 template <int ACT, bool CKPT8>
 struct GateGradProb {
   static constexpr int kAMN = 0, kBMN = 1;
-  static constexpr int kStg = 3 * 4096;
+  static constexpr int kStg = 3 * 2048;
   struct Params {
     int* status;
     PairWalk walk;
@@ -413,19 +433,12 @@ struct GateGradProb {
             pu[2 * j + i] = pack_bf16(du[2 * i], du[2 * i + 1]);
           }
         }
-        if (half == 0) staging_free(e.lane);
-        stage_bf16(e.stg, e.lane, half, ph);
-        stage_bf16(e.stg + 4096, e.lane, half, pg);
-        stage_bf16(e.stg + 8192, e.lane, half, pu);
+        staging_free(e.lane);
+        stage_bf16_32(e.stg, e.lane, ph);
+        stage_bf16_32(e.stg + 2048, e.lane, pg);
+        stage_bf16_32(e.stg + 4096, e.lane, pu);
+        store3(e, c0 + half * 32, y0, P.f);
       }
-      staging_ready();
-      if (e.lane == 0) {
-        tma_store_2d(&e.maps->o[0], e.stg, c0, y0);
-        tma_store_2d(&e.maps->o[1], e.stg + 4096, c0, y0);
-        tma_store_2d(&e.maps->o[2], e.stg + 8192, c0, y0);
-        bulk_commit();
-      }
-      __syncwarp();
     }
   }
 };
@@ -854,10 +867,11 @@ cudaError_t launch_ffn_fwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
   FFN_MAP(map_kmajor(&m.a[0], x, p.N, p.d_in, kPairHalf));
   FFN_MAP(map_b_k(&m, 0, Wg, p.d_ff, p.d_in));
   FFN_MAP(map_b_k(&m, 1, Wu, p.d_ff, p.d_in));
-  FFN_MAP(map_out(&m.o[0], false, ws, p.N, p.d_ff, 64));
-  if (s && !p.ckpt8) {
-    FFN_MAP(map_out(&m.o[1], false, s->g, p.N, p.d_ff, 64));
-    FFN_MAP(map_out(&m.o[2], false, s->u, p.N, p.d_ff, 64));
+  const bool three = s && !p.ckpt8;
+  FFN_MAP(map_out(&m.o[0], false, ws, p.N, p.d_ff, three ? 32 : 64));
+  if (three) {
+    FFN_MAP(map_out(&m.o[1], false, s->g, p.N, p.d_ff, 32));
+    FFN_MAP(map_out(&m.o[2], false, s->u, p.N, p.d_ff, 32));
   }
 #define FFN_GATE(ACT)                                                              \
   FFN_TRY(!s ? run_gate<ACT, false, false>(p, m, s, st)                            \
@@ -883,9 +897,9 @@ cudaError_t launch_ffn_bwd_tc(const FfnPlan& p, const void* x, const void* Wg, c
   PairMaps m{};
   FFN_MAP(map_kmajor(&m.a[0], dy, p.N, p.d_out, kPairHalf));
   FFN_MAP(map_b_mn(&m, 0, Wd, p.d_out, p.d_ff));
-  FFN_MAP(map_out(&m.o[0], false, h, p.N, p.d_ff, 64));
-  FFN_MAP(map_out(&m.o[1], false, dg, p.N, p.d_ff, 64));
-  FFN_MAP(map_out(&m.o[2], false, du, p.N, p.d_ff, 64));
+  FFN_MAP(map_out(&m.o[0], false, h, p.N, p.d_ff, 32));
+  FFN_MAP(map_out(&m.o[1], false, dg, p.N, p.d_ff, 32));
+  FFN_MAP(map_out(&m.o[2], false, du, p.N, p.d_ff, 32));
 #define FFN_GRAD(ACT)                                              \
   FFN_TRY(p.ckpt8 ? run_gate_grad<ACT, true>(p, m, s, st)          \
                   : run_gate_grad<ACT, false>(p, m, s, st))
