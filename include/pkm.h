@@ -394,7 +394,9 @@ pkm_status pkm_shard_scatter_dw(const pkm_dims* d, const int32_t* perm, const fl
  *     g = x Wg^T,  u = x Wu^T,  h = act(g) * u,  y = h Wd^T.
  * Row-major layouts, storage type T = bf16 (fp32 with PKM_F_FP32):
  *     x [N][d_in]   Wg, Wu [d_ff][d_in]   Wd [d_out][d_ff]   y, dy [N][d_out]   dx [N][d_in]
- * d_in, d_ff and d_out are multiples of 8.  N == 0 is a no-op returning PKM_OK.
+ * d_in, d_ff and d_out are multiples of 8 up to 2^20, N <= 2^26 (2^22 with PKM_F_FP32 or
+ * PKM_F_SIMT), N times the largest width <= 2^44; more is PKM_ERR_UNSUPPORTED.  N == 0 is a
+ * no-op returning PKM_OK (no gradient is touched).
  * Products are accumulated in fp32.  With bf16 storage on tensor cores h, dg and du are
  * rounded to bf16 before the product that takes them; with PKM_F_FP32 or PKM_F_SIMT they
  * stay fp32.  flags: PKM_F_FP32, PKM_F_SIMT and the PKM_FFN_* below. */

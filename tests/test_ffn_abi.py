@@ -99,7 +99,9 @@ def test_block_refusals():
     assert _fwd(d, ws=FAKE + 128) == P.PKM_ERR_WORKSPACE
     assert _bwd(d, wsb=P.pkm_ffn_workspace_bytes(d, P.PKM_BWD) - 1) == P.PKM_ERR_WORKSPACE
     assert _fwd(_d(d_ff=(1 << 20) + 8)) == P.PKM_ERR_UNSUPPORTED
-    assert _fwd(_d(N=(1 << 30) + 1)) == P.PKM_ERR_UNSUPPORTED
+    assert _fwd(_d(N=(1 << 26) + 1)) == P.PKM_ERR_UNSUPPORTED
+    assert _fwd(_d(N=(1 << 26), d_ff=1 << 19)) == P.PKM_ERR_UNSUPPORTED
+    assert _bwd(_d(N=(1 << 22) + 1, flags=P.PKM_F_FP32)) == P.PKM_ERR_UNSUPPORTED
     assert _fwd(_d(N=0), x=None, y=None, ws=None, wsb=0) == P.PKM_OK
     assert _bwd(_d(N=0), saved=None, dy=None, ws=None, wsb=0) == P.PKM_OK
     assert P.load().pkm_ffn_forward(None, *[FAKE] * 5, None, FAKE, 1 << 30, None) == bad
