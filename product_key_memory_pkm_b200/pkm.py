@@ -510,29 +510,40 @@ def pkm_shard_scatter_dw(dims: Dims, perm, dw_ret, dw, stream=None) -> None:
 # Unlike the raw-address calls above, these check the tensors they are given: type, shape,
 # contiguity and device (integer addresses pass unchecked).
 
+_torch = None
+
+
 class _Checked:
     """Checks of one call's tensors and the call's stream.  Few-token calls run for a few
-    microseconds on the GPU, so this avoids what costs one on the host: repeated imports and
-    the wrapper objects of torch.cuda.current_stream()."""
+    microseconds on the GPU, so this avoids what costs one on the host: repeated imports, the
+    wrapper objects of torch.cuda.current_stream(), and telling apart what is wrong with a
+    tensor before anything is."""
     __slots__ = ("torch", "device")
 
     def __init__(self):
-        import torch
-        self.torch = torch
-        self.device = None  # the current device, once a GPU tensor has been seen
+        global _torch
+        if _torch is None:
+            import torch
+            _torch = torch
+        self.torch = _torch
+        try:
+            self.device = _torch._C._cuda_getDevice()
+        except (AttributeError, RuntimeError):  # no GPU, or a build without CUDA
+            self.device = -2                    # no tensor is there
 
     def __call__(self, t, name: str, dtype, shape: tuple, optional: bool = False) -> int | None:
         """Address of a contiguous ``shape`` tensor of ``dtype`` on the current device."""
-        if t is None:
-            if optional:
-                return None
-            raise ValueError(f"{name} is missing")
-        if isinstance(t, int):
+        if t is None or isinstance(t, int):
+            if t is None and not optional:
+                raise ValueError(f"{name} is missing")
             return t
+        if (t.dtype is dtype and t.shape == shape and t.is_contiguous()
+                and t.get_device() == self.device):
+            return t.data_ptr()
         if t.dtype != dtype:
             raise TypeError(f"{name}: {dtype} wanted, got {t.dtype}")
         if t.shape != shape:
-            raise ValueError(f"{name}: shape {shape} wanted, got {tuple(t.shape)}")
+            raise ValueError(f"{name}: shape {tuple(shape)} wanted, got {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} is not contiguous")
         self.place(t, name)
@@ -541,13 +552,11 @@ class _Checked:
     def place(self, t, name: str) -> None:
         if not t.is_cuda:
             raise ValueError(f"{name} is not on a GPU")
-        if self.device is None:
-            self.device = self.torch._C._cuda_getDevice()
         if t.get_device() != self.device:
             raise ValueError(f"{name} is on {t.device}, the current device is {self.device}")
 
     def stream(self, stream):
-        if stream is None and self.device is not None:
+        if stream is None and self.device >= 0:
             return self.torch._C._cuda_getCurrentRawStream(self.device)
         return _stream(stream)
 
@@ -579,8 +588,8 @@ class FfnDims:
 
     @property
     def dtype(self):
-        import torch
-        return torch.float32 if self.flags & PKM_F_FP32 else torch.bfloat16
+        t = _Checked().torch if _torch is None else _torch
+        return t.float32 if self.flags & PKM_F_FP32 else t.bfloat16
 
     @property
     def runs(self) -> int:
@@ -710,8 +719,8 @@ def _w4(ck: _Checked, W, name: str, d_out: int, d_in: int, group: int) -> pkm_w4
     if group <= 0:
         raise ValueError(f"group: a positive multiple of 32 wanted, got {group}")
     codes, scale = W
-    return pkm_w4(ck(codes, f"{name} codes", ck.torch.uint8, (d_out, d_in // 2)),
-                  ck(scale, f"{name} scale", ck.torch.bfloat16, (d_out, -(-d_in // group))))
+    return pkm_w4(ck(codes, name, ck.torch.uint8, (d_out, d_in // 2)),
+                  ck(scale, name, ck.torch.bfloat16, (d_out, -(-d_in // group))))
 
 
 def _matrix(ck: _Checked, t, name: str):
