@@ -102,7 +102,13 @@ struct W4Unit {
       next_s = to * sh.ng;
     }
   };
-  __device__ static int col(int u, int c, int j) { return u * kCols + 8 * WORDS * c + 8 * j; }
+  // Lanes 2 and 3 take four words in the order 1, 0, 3, 2, so that the four lanes' columns of x lie
+  // in different banks of shared memory (which columns meet in one instruction is of no
+  // consequence).  The choice is made where a word is used: at the load it would wait for it.
+  __device__ static bool swapped(int c) { return WORDS == 4 && (c & 2); }
+  __device__ static int col(int u, int c, int j) {
+    return u * kCols + 8 * WORDS * c + 8 * (swapped(c) ? j ^ 1 : j);
+  }
   __device__ void load(const Src& S, const W4Shape& sh, int u, int c) {
     // a lane past the row's end reads within the row: its x is zero, and no code is NaN
     const int at = u * (kCols / 2);
@@ -128,10 +134,11 @@ struct W4Unit {
   struct A {
     uint32_t g[4], h[4];
   };
-  __device__ A operands(int j) const {
+  __device__ A operands(int c, int j) const {
+    constexpr int x = WORDS == 4 ? 1 : 0;
     A o;
-    w4_pairs(w[0][j], o.g);
-    w4_pairs(w[1][j], o.h);
+    w4_pairs(swapped(c) ? w[0][j ^ x] : w[0][j], o.g);
+    w4_pairs(swapped(c) ? w[1][j ^ x] : w[1][j], o.h);
     return o;
   }
   // t = a word's products with 8 tokens, x their columns; then acc += scale * t
@@ -179,7 +186,7 @@ struct W16Unit {
   struct A {
     uint4 g, h;
   };
-  __device__ A operands(int j) const { return A{w[0][j], w[1][j]}; }
+  __device__ A operands(int, int j) const { return A{w[0][j], w[1][j]}; }
   __device__ static void mac(float (&t)[4], const A& o, const uint4& x) {
     mma16816_first(t, o.g.x, o.h.x, o.g.y, o.h.y, x.x, x.y);
     mma16816(t, o.g.z, o.h.z, o.g.w, o.h.w, x.z, x.w);
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(kTpb, Depth<Unit, M, NT>::ctas)
           for (int j = 0; j < Unit::kWords; ++j) {
             typename Unit::A a[M];
 #pragma unroll
-            for (int m = 0; m < M; ++m) a[m] = w[m][b].operands(j);
+            for (int m = 0; m < M; ++m) a[m] = w[m][b].operands(c, j);
             const int k = Unit::col(v, c, j);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -391,9 +398,9 @@ __global__ void __launch_bounds__(kTpb, Depth<Unit, M, NT>::ctas)
 // shared memory and each of its warps takes 16 rows through all of k.  Rows are dealt so that they
 // fill whole rounds of the SMs with as many warps as fit, up to 24: a warp's products depend on
 // one another, and other warps and kWideIlp products at a time fill the gaps.  Against 50264 x
-// 1600: 24 us for 16 tokens (few_kernel 39), 33 for 32 (89), 58 for 64 (140); for 8 tokens both
-// take 20 to 22, so those stay there.  Still bound by the latency of that chain: the weights
-// alone would take 6.6 us, issuing all products about 20.
+// 1600: 24 us for 16 tokens (few_kernel 39), 33 for 32 (89), 55 for 64 (140); for 8 tokens both
+// take 20 to 24, so those stay there.  Still bound by the latency of that chain and of the reads
+// of x: the weights alone would take 6.6 us, issuing all products about 20.
 constexpr int kWideRows = 16, kWideWarps = 24, kWideIlp = 2;
 constexpr int kWideSmem = 225 * 1024;
 
@@ -416,10 +423,9 @@ __global__ void __launch_bounds__(32 * kWideWarps, 1)
   extern __shared__ __align__(16) unsigned char xs[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  // The 8 lanes that read 16 bytes at a time are two rows' four columns 16 * WORDS bytes apart: a
-  // pitch of 64, 16, 32 bytes past a multiple of 128 keeps them on different banks for 1 and 2
-  // words, and to two turns for 4.  (Lanes 2 and 3 taking their 4 words in another order avoids the
-  // second turn and measured the same.)
+  // The 8 lanes that read 16 bytes at a time are two rows' four columns 16 * WORDS bytes apart (4
+  // words: two pairs of neighbours, see Unit::col): a pitch of 64, 16, 32 bytes past a multiple of
+  // 128 keeps them on different banks for 1, 2, 4 words.
   const int pitch = chunk * 2 + wide_pad(WORDS);
   const int tiles = (sh.d_out + kWideRows - 1) / kWideRows;
   const int chunks = (sh.d_in + chunk - 1) / chunk;
@@ -463,7 +469,7 @@ __global__ void __launch_bounds__(32 * kWideWarps, 1)
           if (u + i >= u1) break;
 #pragma unroll
           for (int j = 0; j < WORDS; ++j) {
-            const typename Unit::A a = w[i].operands(j);
+            const typename Unit::A a = w[i].operands(c, j);
             const unsigned char* xj = xb + Unit::col(u + i - u0, c, j) * 2;
             // scaled word by word: no registers for the sums of a whole unit; kIlp products at a
             // time, since each waits for the one before it
