@@ -1,7 +1,7 @@
 """Thin Python binding of the C ABI in ``include/pkm.h`` (ctypes).
 
-Argument marshalling only: every step of the layer runs in the CUDA kernels of
-``libpkm_b200.so``.  PyTorch is used for device memory and streams.  There is no
+Argument marshalling only (the feed-forward, checkpoint and 4-bit functions also check
+the tensors they get): every step runs in the CUDA kernels of ``libpkm_b200.so``.  PyTorch is used for device memory and streams.  There is no
 CPU fallback: loading fails loudly when the library has not been built.
 
 The functions carry the C names (``pkm_forward``, ``pkm_backward``,
