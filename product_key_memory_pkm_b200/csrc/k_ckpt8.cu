@@ -6,7 +6,7 @@
 // and a thread has kUnroll such chunks in flight.  bf16, 16384 x 6400: unpack 51 us (6.4 TB/s),
 // pack 62 us (5.3 TB/s; it issues instructions in four of five cycles, about 110 per chunk, of
 // which the exact halves cost 3 per value).
-#include <algorithm>
+#include <type_traits>
 #include <type_traits>
 
 #include "ffn_internal.cuh"

@@ -54,6 +54,21 @@ def test_checkpoint_round_trip(rows, cols, dtype):
         assert torch.equal(v, want.to(out))
 
 
+@pytest.mark.parametrize("cols", [3200, 3208])
+def test_checkpoint_offsets_beyond_32_bits(cols):
+    rows = (1 << 31) // cols + 100
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-50:] = rnd(1, 50, cols).bfloat16()
+    codes, scale = P.alloc_ckpt8(rows, cols)
+    P.pkm_ckpt8_pack(x, codes, scale)
+    wc, ws = R.pack8(x[-60:])
+    assert torch.equal(codes[-60:], wc) and torch.equal(scale[-60:], ws)
+    x[-50:] = 0
+    P.pkm_ckpt8_unpack(codes, scale, x)
+    want = (wc.float() * ws.repeat_interleave(32, 1))[:, :cols].bfloat16()
+    assert torch.equal(x[-60:], want)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_checkpoint_halves_go_to_the_even_code(dtype):
     """Runs whose values lie exactly between two codes, and one step to either side of it."""

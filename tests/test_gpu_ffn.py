@@ -131,6 +131,77 @@ def test_few_tokens(n):
     assert (whole[n:] == 7.0).all()
 
 
+@pytest.mark.parametrize("mode", ["fp32", "fp32-ckpt8", "simt", "simt-ckpt8"])
+def test_cuda_core_path_of_large_products(mode):
+    """Beyond 2^29 multiplications a product the CUDA-core path takes its large tiles and separate
+    elementwise kernels."""
+    n, di, f, do = 1100, 1032, 520, 264
+    assert n * f * di > 1 << 29
+    dtype = torch.float32 if mode.startswith("fp32") else torch.bfloat16
+    flags = (P.PKM_F_SIMT if mode.startswith("simt") else 0) | (
+        P.PKM_FFN_CKPT8 if mode.endswith("ckpt8") else 0)
+    act = "gelu" if mode.endswith("ckpt8") else "silu"
+    d = dims(n, di, f, do, dtype, act, flags)
+    t, dy = make(n, di, f, do, dtype, seed=12)
+    whole, y = guarded(n, do, dtype)
+    saved, rms = P.alloc_ffn_saved(d), TWO if dtype == torch.bfloat16 else None
+    P.pkm_ffn_forward(d, **t, y=y, saved=saved, workspace=scratch(d, P.PKM_FWD))
+    check_forward(d, t, act, saved, y, rms)
+    assert (whole[n:] == 7.0).all()
+    check_backward(d, t, act, saved, dy, run_backward(d, t, saved, dy), R.roundoff(dtype), rms)
+    if dtype == torch.bfloat16:
+        db = dims(n, di, f, do, dtype, act, flags | P.PKM_FFN_GRAD_BF16)
+        out = run_backward(db, t, saved, dy, {"d" + k: torch.full_like(t[k], 5.0)
+                                              for k in ("Wg", "Wu", "Wd")})
+        check_backward(db, t, act, saved, dy, out, 2.0 ** -8, TWO)
+
+
+@pytest.mark.parametrize("mode", ["bf16", "bf16-ckpt8", "fp32"])
+def test_offsets_beyond_32_bits(mode):
+    """More than 2^31 kept values: the last tokens' rows are right, and so is a weight gradient
+    that only they feed."""
+    n, di, f, do = 336_000, 64, 6400, 64
+    assert n * f > 1 << 31
+    dtype = torch.float32 if mode == "fp32" else torch.bfloat16
+    d = dims(n, di, f, do, dtype, "silu", P.PKM_FFN_CKPT8 if mode.endswith("ckpt8") else 0)
+    t, dy = make(n, di, f, do, dtype, seed=1)
+    last = slice(n - 70, n)
+    dy[:n - 70] = 0
+    y, saved = torch.empty(n, do, dtype=dtype, device="cuda"), P.alloc_ffn_saved(d)
+    P.pkm_ffn_forward(d, **t, y=y, saved=saved, workspace=scratch(d, P.PKM_FWD))
+    tail = {**t, "x": t["x"][last]}
+    kept = {k: None if v is None else v[last] for k, v in saved.items()}
+    rms = TWO if dtype == torch.bfloat16 else None
+    check_forward(d, tail, "silu", kept, y[last], rms)
+    out = run_backward(d, t, saved, dy)
+    assert (out["dx"][:n - 70] == 0).all()
+    out["dx"] = out["dx"][last]
+    check_backward(d, tail, "silu", kept, dy[last], out, R.roundoff(dtype), rms)
+    assert P.pkm_check_status() == P.PKM_OK
+
+
+def test_the_current_stream_is_used():
+    """Without a stream argument the calls go to torch's current stream."""
+    n, di, f, do = 12, 256, 520, 136
+    d = dims(n, di, f, do, torch.bfloat16)
+    t, dy = make(n, di, f, do, torch.bfloat16, seed=3)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y, saved = torch.empty_like(dy), P.alloc_ffn_saved(d)
+        a = torch.randn(8192, 8192, device="cuda")
+        for _ in range(20):
+            a = a @ a * 1e-4          # the side stream is busy: a call elsewhere would overtake x
+        t["x"] = (t["x"].float() + a[:n, :di] * 0).bfloat16()
+        P.pkm_ffn_forward(d, **t, y=y, saved=saved, workspace=scratch(d, P.PKM_FWD))
+        codes, scale = P.alloc_ckpt8(n, do)
+        P.pkm_ckpt8_pack(y, codes, scale)
+    side.synchronize()
+    check_forward(d, t, "silu", saved, y, TWO)
+    wc, ws = R.pack8(y)
+    assert torch.equal(codes, wc) and torch.equal(scale, ws)
+
+
 def offset16(t):
     """The same values at an address that is a multiple of 16 and of no more."""
     per = 16 // t.element_size()
