@@ -399,7 +399,10 @@ pkm_status pkm_shard_scatter_dw(const pkm_dims* d, const int32_t* perm, const fl
  * no-op returning PKM_OK (no gradient is touched).
  * Products are accumulated in fp32.  With bf16 storage on tensor cores h, dg and du are
  * rounded to bf16 before the product that takes them; with PKM_F_FP32 or PKM_F_SIMT they
- * stay fp32.  flags: PKM_F_FP32, PKM_F_SIMT and the PKM_FFN_* below. */
+ * stay fp32.  flags: PKM_F_FP32, PKM_F_SIMT and the PKM_FFN_* below.
+ * In this and the next two sections a call's outputs and its workspace share no bytes with each
+ * other or with its inputs (checked: PKM_ERR_INVALID_ARG).  Inputs may be the same buffer; tied
+ * weights get a gradient buffer each. */
 #define PKM_ACT_SILU 0 /* v / (1 + exp(-v)) */
 #define PKM_ACT_GELU 1 /* v Phi(v), Phi the normal distribution function (no approximation) */
 

@@ -93,6 +93,29 @@ pkm_status check_workspace(size_t need, const void* ws, size_t bytes) {
   return PKM_OK;
 }
 
+// A buffer of a call.  The kernels of one call read and write in no promised order, so its outputs
+// (the first `outs` buffers; the workspace is one) may share no bytes with each other or with what
+// it reads.
+struct Span {
+  const void* p;
+  size_t n;
+};
+template <int COUNT>
+pkm_status check_apart(const Span (&s)[COUNT], int outs) {
+  for (int i = 0; i < outs; ++i) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].p);
+    for (int j = i + 1; j < COUNT; ++j) {
+      const uintptr_t b = reinterpret_cast<uintptr_t>(s[j].p);
+      if (a && b && (a <= b ? b - a < s[i].n : a - b < s[j].n)) return PKM_ERR_INVALID_ARG;
+    }
+  }
+  return PKM_OK;
+}
+size_t w4_codes_bytes(int32_t d_out, int32_t d_in) { return (size_t)d_out * (d_in / 2); }
+size_t w4_scale_bytes(int32_t d_out, int32_t d_in, int32_t group) {
+  return (size_t)d_out * (((int64_t)d_in + group - 1) / group) * 2;
+}
+
 pkm_status check_saved(const FfnPlan& p, const pkm_ffn_saved* s) {
   if (!s) return PKM_ERR_INVALID_ARG;
   PKM_NEED(s->g);
@@ -159,7 +182,21 @@ pkm_status pkm_ffn_forward(const pkm_ffn_dims* d, const void* x, const void* Wg,
   if (d->N == 0) return PKM_OK;
   PKM_NEED(x); PKM_NEED(Wg); PKM_NEED(Wu); PKM_NEED(Wd); PKM_NEED(y);
   if (saved) PKM_TRY(check_saved(shape_plan(d), saved));
-  PKM_TRY(check_workspace(pkm_ffn_workspace_bytes(d, PKM_FWD), workspace, workspace_bytes));
+  const size_t need = pkm_ffn_workspace_bytes(d, PKM_FWD);
+  PKM_TRY(check_workspace(need, workspace, workspace_bytes));
+  const size_t e = d->flags & PKM_F_FP32 ? 4 : 2, in = (size_t)d->d_ff * d->d_in * e;
+  const size_t kept = saved ? pkm_ffn_saved_bytes(d, PKM_FFN_SAVED_G) : 0;
+  const size_t scales = saved ? pkm_ffn_saved_bytes(d, PKM_FFN_SAVED_G_SCALE) : 0;
+  PKM_TRY(check_apart<10>({{y, (size_t)d->N * d->d_out * e},
+                           {workspace, need},
+                           {saved ? saved->g : nullptr, kept},
+                           {saved ? saved->u : nullptr, kept},
+                           {scales ? saved->g_scale : nullptr, scales},
+                           {scales ? saved->u_scale : nullptr, scales},
+                           {x, (size_t)d->N * d->d_in * e},
+                           {Wg, in},
+                           {Wu, in},
+                           {Wd, (size_t)d->d_out * d->d_ff * e}}, 6));
   FfnPlan p;
   PKM_TRY(make_plan(d, &p));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -179,7 +216,27 @@ pkm_status pkm_ffn_backward(const pkm_ffn_dims* d, const void* x, const void* Wg
   PKM_NEED(x); PKM_NEED(Wg); PKM_NEED(Wu); PKM_NEED(Wd); PKM_NEED(dy);
   PKM_TRY(check_saved(shape_plan(d), saved));
   PKM_OPT(dx); PKM_OPT(dWg); PKM_OPT(dWu); PKM_OPT(dWd);
-  PKM_TRY(check_workspace(pkm_ffn_workspace_bytes(d, PKM_BWD), workspace, workspace_bytes));
+  const size_t need = pkm_ffn_workspace_bytes(d, PKM_BWD);
+  PKM_TRY(check_workspace(need, workspace, workspace_bytes));
+  const size_t e = d->flags & PKM_F_FP32 ? 4 : 2, ge = d->flags & PKM_FFN_GRAD_BF16 ? 2 : 4;
+  const size_t xs = (size_t)d->N * d->d_in, in = (size_t)d->d_ff * d->d_in,
+               out = (size_t)d->d_out * d->d_ff;
+  const size_t kept = pkm_ffn_saved_bytes(d, PKM_FFN_SAVED_G);
+  const size_t scales = pkm_ffn_saved_bytes(d, PKM_FFN_SAVED_G_SCALE);
+  PKM_TRY(check_apart<14>({{dx, xs * e},
+                           {dWg, in * ge},
+                           {dWu, in * ge},
+                           {dWd, out * ge},
+                           {workspace, need},
+                           {x, xs * e},
+                           {Wg, in * e},
+                           {Wu, in * e},
+                           {Wd, out * e},
+                           {saved->g, kept},
+                           {saved->u, kept},
+                           {scales ? saved->g_scale : nullptr, scales},
+                           {scales ? saved->u_scale : nullptr, scales},
+                           {dy, (size_t)d->N * d->d_out * e}}, 5));
   FfnPlan p;
   PKM_TRY(make_plan(d, &p));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -192,6 +249,10 @@ pkm_status pkm_ckpt8_pack(int64_t rows, int32_t cols, uint32_t flags, const void
   PKM_TRY(validate_ckpt8(rows, cols, flags));
   if (rows == 0) return PKM_OK;
   PKM_NEED(src); PKM_NEED(codes); PKM_NEED(scale);
+  const size_t runs = (size_t)rows * ckpt_runs(cols);
+  PKM_TRY(check_apart<3>({{codes, runs * kCkptRun},
+                          {scale, runs * 4},
+                          {src, (size_t)rows * cols * (flags & PKM_F_FP32 ? 4 : 2)}}, 2));
   DeviceInfo info;
   if (!current_device(&info)) return PKM_ERR_CUDA;
   return cuda_status(launch_ckpt8_pack(rows, cols, flags & PKM_F_FP32, src, codes, scale,
@@ -203,6 +264,10 @@ pkm_status pkm_ckpt8_unpack(int64_t rows, int32_t cols, uint32_t flags, const in
   PKM_TRY(validate_ckpt8(rows, cols, flags));
   if (rows == 0) return PKM_OK;
   PKM_NEED(codes); PKM_NEED(scale); PKM_NEED(dst);
+  const size_t runs = (size_t)rows * ckpt_runs(cols);
+  PKM_TRY(check_apart<3>({{dst, (size_t)rows * cols * (flags & PKM_F_FP32 ? 4 : 2)},
+                          {codes, runs * kCkptRun},
+                          {scale, runs * 4}}, 1));
   DeviceInfo info;
   if (!current_device(&info)) return PKM_ERR_CUDA;
   return cuda_status(launch_ckpt8_unpack(rows, cols, flags & PKM_F_FP32, codes, scale, dst,
@@ -213,6 +278,9 @@ pkm_status pkm_w4_pack(int32_t d_out, int32_t d_in, int32_t group, const void* W
                        void* scale, void* stream) {
   PKM_TRY(validate_w4(d_out, d_in, group));
   PKM_NEED(W); PKM_NEED(codes); PKM_NEED(scale);
+  PKM_TRY(check_apart<3>({{codes, w4_codes_bytes(d_out, d_in)},
+                          {scale, w4_scale_bytes(d_out, d_in, group)},
+                          {W, (size_t)d_out * d_in * 2}}, 2));
   DeviceInfo info;
   if (!current_device(&info)) return PKM_ERR_CUDA;
   return cuda_status(
@@ -225,6 +293,9 @@ pkm_status pkm_w4_unpack(int32_t d_out, int32_t d_in, int32_t group, const pkm_w
   W4Mat m;
   PKM_TRY(check_w4(W, &m));
   PKM_NEED(out);
+  PKM_TRY(check_apart<3>({{out, (size_t)d_out * d_in * 2},
+                          {W->codes, w4_codes_bytes(d_out, d_in)},
+                          {W->scale, w4_scale_bytes(d_out, d_in, group)}}, 1));
   DeviceInfo info;
   if (!current_device(&info)) return PKM_ERR_CUDA;
   return cuda_status(
@@ -240,6 +311,10 @@ pkm_status pkm_w4_matvec(int64_t N, int32_t d_in, int32_t d_out, int32_t group, 
   PKM_NEED(x); PKM_NEED(y);
   W4Mat m;
   PKM_TRY(check_w4(W, &m));
+  PKM_TRY(check_apart<4>({{y, (size_t)N * d_out * 4},
+                          {x, (size_t)N * d_in * 2},
+                          {W->codes, w4_codes_bytes(d_out, d_in)},
+                          {W->scale, w4_scale_bytes(d_out, d_in, group)}}, 1));
   DeviceInfo info;
   if (!current_device(&info)) return PKM_ERR_CUDA;
   return cuda_status(launch_w4_matvec(N, d_in, d_out, group, x, m, y, info.sm_count,
@@ -260,7 +335,20 @@ pkm_status pkm_w4_ffn(const pkm_ffn_dims* d, int32_t group, const void* x, const
   PKM_TRY(check_w4(Wg, &g));
   PKM_TRY(check_w4(Wu, &u));
   PKM_TRY(check_w4(Wd, &o));
-  PKM_TRY(check_workspace(pkm_ffn_workspace_bytes(d, PKM_FWD), workspace, workspace_bytes));
+  const size_t need = pkm_ffn_workspace_bytes(d, PKM_FWD);
+  PKM_TRY(check_workspace(need, workspace, workspace_bytes));
+  const size_t cin = w4_codes_bytes(d->d_ff, d->d_in), cout = w4_codes_bytes(d->d_out, d->d_ff);
+  const size_t sin = w4_scale_bytes(d->d_ff, d->d_in, group);
+  const size_t sout = w4_scale_bytes(d->d_out, d->d_ff, group);
+  PKM_TRY(check_apart<9>({{y, (size_t)d->N * d->d_out * 2},
+                          {workspace, need},
+                          {x, (size_t)d->N * d->d_in * 2},
+                          {Wg->codes, cin},
+                          {Wg->scale, sin},
+                          {Wu->codes, cin},
+                          {Wu->scale, sin},
+                          {Wd->codes, cout},
+                          {Wd->scale, sout}}, 2));
   FfnPlan p;
   PKM_TRY(make_plan(d, &p));
   return cuda_status(

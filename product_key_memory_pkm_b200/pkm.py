@@ -1,8 +1,9 @@
 """Thin Python binding of the C ABI in ``include/pkm.h`` (ctypes).
 
 Argument marshalling only (the feed-forward, checkpoint and 4-bit functions also check
-the tensors they get): every step runs in the CUDA kernels of ``libpkm_b200.so``.  PyTorch is used for device memory and streams.  There is no
-CPU fallback: loading fails loudly when the library has not been built.
+the tensors they get): every step runs in the CUDA kernels of ``libpkm_b200.so``.
+PyTorch is used for device memory and streams.  There is no CPU fallback: loading fails
+loudly when the library has not been built.
 
 The functions carry the C names (``pkm_forward``, ``pkm_backward``,
 ``pkm_query``, ``pkm_subkey_scores``, ``pkm_candidate_topk``,
@@ -566,6 +567,8 @@ class _Checked:
         if not workspace.is_contiguous():
             raise ValueError("workspace is not contiguous")
         self.place(workspace, "workspace")
+        if workspace_bytes > workspace.nbytes:
+            raise ValueError(f"workspace has {workspace.nbytes} bytes, not {workspace_bytes}")
         return workspace.data_ptr(), workspace_bytes or workspace.nbytes
 
 

@@ -156,6 +156,86 @@ def test_w4_refusals():
     assert ffn(_d(N=0, d_ff=96), ws=None, wsb=0) == P.PKM_OK
 
 
+def _apart(*names):
+    """Addresses far enough apart for every buffer of the small calls below."""
+    return {n: (i + 1) << 24 for i, n in enumerate(names)}
+
+
+FWD = ("x", "Wg", "Wu", "Wd", "y", "g", "u", "sg", "su", "ws")
+BWD = FWD[:4] + ("g", "u", "sg", "su", "dy", "dx", "dWg", "dWu", "dWd", "ws")
+
+
+def _call_block(L, d, a, which):
+    s = ctypes.byref(P.pkm_ffn_saved(a["g"], a["u"], a["sg"], a["su"]))
+    if which == P.PKM_FWD:
+        return L.pkm_ffn_forward(ctypes.byref(d.c()), *(a[k] for k in FWD[:5]), s, a["ws"],
+                                 1 << 20, None)
+    return L.pkm_ffn_backward(ctypes.byref(d.c()), *(a[k] for k in FWD[:4]), s,
+                              *(a[k] for k in BWD[8:13]), a["ws"], 1 << 20, None)
+
+
+@pytest.mark.parametrize("flags", [0, P.PKM_FFN_CKPT8, P.PKM_F_FP32])
+@pytest.mark.parametrize("which", [P.PKM_FWD, P.PKM_BWD])
+def test_outputs_that_share_bytes_are_refused(which, flags):
+    """Every output against every other buffer: the same address, and the last bytes only."""
+    d = _d(flags=flags)
+    names, outs = (FWD, FWD[4:]) if which == P.PKM_FWD else (BWD, BWD[9:])
+    scales = ("sg", "su")
+    esz = 4 if flags & P.PKM_F_FP32 else 2
+    size = dict(x=64 * 64 * esz, y=64 * 72 * esz, dy=64 * 72 * esz, dx=64 * 64 * esz,
+                Wg=136 * 64 * esz, Wu=136 * 64 * esz, Wd=72 * 136 * esz, dWg=136 * 64 * 4,
+                dWu=136 * 64 * 4, dWd=72 * 136 * 4, ws=P.pkm_ffn_workspace_bytes(d, which),
+                g=P.pkm_ffn_saved_bytes(d, "g"), u=P.pkm_ffn_saved_bytes(d, "u"),
+                sg=P.pkm_ffn_saved_bytes(d, "g_scale"), su=P.pkm_ffn_saved_bytes(d, "u_scale"))
+    L = P.load()
+    for o in outs:
+        for n in names:
+            if n == o or not flags & P.PKM_FFN_CKPT8 and (n in scales or o in scales):
+                continue
+            a = _apart(*names)
+            assert _call_block(L, d, {**a, o: a[n]}, which) == P.PKM_ERR_INVALID_ARG, (o, n)
+            if o != "ws":  # whose alignment is larger
+                last = a[n] + (size[n] - 1) // 16 * 16
+                assert _call_block(L, d, {**a, o: last}, which) == P.PKM_ERR_INVALID_ARG, (o, n)
+    if not torch.cuda.is_available():
+        # tied weights and neighbouring buffers pass the checks (and end where a GPU is needed)
+        a = _apart(*names)
+        assert _call_block(L, d, {**a, "Wu": a["Wg"]}, which) == P.PKM_ERR_CUDA
+        for o in set(outs) - {"ws"}:
+            for n in set(names) - {o}:
+                nxt = a[n] + (size[n] + 15) // 16 * 16
+                assert _call_block(L, d, {**a, o: nxt}, which) == P.PKM_ERR_CUDA, (o, n)
+
+
+def test_packing_and_products_in_place_are_refused():
+    L, bad = P.load(), P.PKM_ERR_INVALID_ARG
+    a, b, c, e = ((i + 1) << 24 for i in range(4))
+    for p in ((a, a, b), (a, b, a), (a, b, b), (a, a + 16, b)):
+        assert L.pkm_ckpt8_pack(4, 64, 0, *p, None) == bad
+        assert L.pkm_w4_pack(8, 64, 32, *p, None) == bad
+    for p in ((a, b, a), (a, b, b), (a, b, a + 16)):
+        assert L.pkm_ckpt8_unpack(4, 64, 0, *p, None) == bad
+        assert L.pkm_w4_unpack(8, 64, 32, ctypes.byref(P.pkm_w4(*p[:2])), p[2], None) == bad
+    for x, y in ((a, a), (a, b), (a, c), (a, a + 16)):
+        assert L.pkm_w4_matvec(4, 64, 8, 32, x, ctypes.byref(P.pkm_w4(b, c)), y, None) == bad
+    d, W = _d(N=8, d_ff=96), ctypes.byref(P.pkm_w4(b, c))
+    for y, ws in ((a, e), (b, e), (c, e), (e, e), (e, a), (e, b), (e, c)):
+        assert L.pkm_w4_ffn(ctypes.byref(d.c()), 32, a, W, W, W, y, ws, 1 << 20, None) == bad
+
+
+def test_workspace_bytes_beyond_the_tensor_are_refused():
+    class Anywhere(P._Checked):
+        __slots__ = ()
+
+        def place(self, t, name):
+            pass
+
+    ws = torch.empty(256, dtype=torch.uint8)
+    assert Anywhere().workspace(ws, 128) == (ws.data_ptr(), 128)
+    with pytest.raises(ValueError, match="256 bytes"):
+        Anywhere().workspace(ws, 512)
+
+
 def test_binding_checks_its_tensors():
     """Wrong type, shape, order or place is refused before the library is called."""
     d = _d(N=2)
