@@ -242,8 +242,7 @@ struct Depth<W16Unit, M, NT> {
 
 template <class Unit, class Mat, class Shape, int M, int NT, Few OUT, int ACT>
 __global__ void __launch_bounds__(kTpb, Depth<Unit, M, NT>::ctas)
-    few_kernel(int N, Shape sh, int ks, const bf* __restrict__ x, Mat W0, Mat W1,
-               void* __restrict__ out, bool first) {
+    few_kernel(int N, Shape sh, int ks, const bf* x, Mat W0, Mat W1, void* out, bool first) {
   const int d_in = sh.d_in, d_out = sh.d_out;
   constexpr int kTileRows = OUT == Few::kGate ? kRows : M * kRows;
   constexpr int kNext = OUT == Few::kGate ? 0 : kRows;  // rows from the first block to the second
@@ -274,7 +273,10 @@ __global__ void __launch_bounds__(kTpb, Depth<Unit, M, NT>::ctas)
 #pragma unroll
   for (int n = 0; n < NT; ++n) xp[n] = x + (int64_t)min(n * 8 + g, N - 1) * d_in;
 
-  // weights do not depend on the kernel before, x of the second product does
+  // Weights do not depend on the kernel before, x of the second product does: that kernel may still
+  // be writing it while this one runs up to the wait.  So x is not __restrict__: loads of such a
+  // pointer to const may take the read-only path, whose data may not change while a kernel runs,
+  // and may be moved ahead of the wait.
   fetch(u0);
   if (first)
     allow_dependent_launch();

@@ -276,3 +276,22 @@ def test_reference_gradients_against_differences(act):
         diff = (side[0] - side[1]) / (2 * eps)
         # the difference's own error: eps^2 times the third derivative (order 1e3 here at most)
         assert abs((diff - (gr[grad][0] * v).sum()).item()) <= 1e-7 * (1 + abs(diff.item()))
+
+
+def test_kernels_that_wait_for_their_producer_take_no_restrict_pointers():
+    """A kernel of the block that starts before its producer has ended reads what that one is still
+    writing.  Loads of a __restrict__ pointer to const may take the read-only path, which allows no
+    such writer, and need not stay behind the wait."""
+    import os
+    import re
+    seen = []
+    for name in ("k_few.cu", "k_ffn_simt.cu", "k_ffn_tc.cu"):
+        with open(os.path.join(B.CSRC, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for kernel in text.split("__global__")[1:]:
+            head, body = kernel.split("{", 1)
+            body = body.split("\n}\n", 1)[0]
+            if "grid_dependency_wait()" in body:
+                seen.append(re.findall(r"(\w+)\s*\(", head)[-1])
+                assert "__restrict__" not in head, seen[-1]
+    assert seen == ["few_kernel", "small_jobs_kernel", "sum_parts_kernel"]

@@ -454,3 +454,38 @@ def test_memory_layer_then_block_with_checkpointed_inputs():
     rel = (got["ckpt"][0].double() - dq_abs).norm() / dq_abs.norm()
     assert rel <= step.norm() / x.double().norm()
     assert P.pkm_check_status() == P.PKM_OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "w4"])
+@pytest.mark.parametrize("n", [1, 8, 16])
+def test_few_token_calls_back_to_back_read_their_own_inner_values(n, kind):
+    """Calls of two inputs in turn through one workspace: each result is its own input's, although
+    the second kernel of a call starts while the first still writes what it reads."""
+    di, f, do, group = 1600, 1056, 264, 32
+    t, _ = make(n, di, f, do, torch.bfloat16, seed=n)
+    xs = [t.pop("x"), torch.randn(n, di, device="cuda").bfloat16()]
+    d = dims(n, di, f, do, torch.bfloat16)
+    ws = scratch(d, P.PKM_FWD)
+    if kind == "w4":
+        packed = {k: P.alloc_w4(*W.shape, group) for k, W in t.items()}
+        for k, W in t.items():
+            P.pkm_w4_pack(W, *packed[k], group=group)
+
+    def call(x, y):
+        if kind == "w4":
+            P.pkm_w4_ffn(d, x, packed["Wg"], packed["Wu"], packed["Wd"], y, group=group, workspace=ws)
+        else:
+            P.pkm_ffn_forward(d, x, t["Wg"], t["Wu"], t["Wd"], y, workspace=ws)
+
+    want = []
+    for x in xs:
+        y = torch.empty(n, do, dtype=torch.bfloat16, device="cuda")
+        call(x, y)
+        torch.cuda.synchronize()
+        want.append(y)
+    assert not torch.equal(*want)
+    got = torch.zeros(200, n, do, dtype=torch.bfloat16, device="cuda")
+    for i in range(200):
+        call(xs[i & 1], got[i])
+    for i in range(200):
+        assert torch.equal(got[i], want[i & 1]), i
