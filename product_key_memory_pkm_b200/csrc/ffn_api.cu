@@ -113,7 +113,7 @@ pkm_status check_apart(const Span (&s)[COUNT], int outs) {
 }
 size_t w4_codes_bytes(int32_t d_out, int32_t d_in) { return (size_t)d_out * (d_in / 2); }
 size_t w4_scale_bytes(int32_t d_out, int32_t d_in, int32_t group) {
-  return (size_t)d_out * (((int64_t)d_in + group - 1) / group) * 2;
+  return (size_t)d_out * w4_groups(d_in, group) * 2;
 }
 
 pkm_status check_saved(const FfnPlan& p, const pkm_ffn_saved* s) {

@@ -167,6 +167,9 @@ struct W4Mat {
   const uint8_t* codes;
   const __nv_bfloat16* scale;
 };
+// Scales of a row.  In 64 bits: any positive multiple of 32 is a group, and d_in + group passes
+// 2^31 for the largest (which then are one group a row).
+inline int w4_groups(int d_in, int group) { return (int)(((int64_t)d_in + group - 1) / group); }
 
 // CUDA-core path (any storage type).
 size_t ffn_simt_workspace(const FfnPlan& p, bool backward);

@@ -76,10 +76,11 @@ struct W4Shape {
   static int words(int group) { return group % 128 == 0 ? 4 : group % 64 == 0 ? 2 : 1; }
   static W4Shape of(int d_in, int d_out, int group) {
     const uint32_t per = (uint32_t)(group / (32 * words(group)));
-    return W4Shape{d_in, d_out, (d_in + group - 1) / group,
+    return W4Shape{d_in, d_out, w4_groups(d_in, group),
                    per == 1 ? 0u : (uint32_t)(((uint64_t)1 << 32) / per + 1)};
   }
-  // i / per for i < 2^15, per <= 2^15: the error of magic, below per, adds i * per / 2^32 < 1/4
+  // i / per for i < 2^15: magic is above 2^32 / per by 1 at most, which adds i / 2^32 < 2^-17 to
+  // the quotient, and that is 1 / per >= 2^-15 below the next integer, or i / per <= 1 - 2^-15.
   __device__ int group_of(int i) const { return magic ? (int)__umulhi((uint32_t)i, magic) : i; }
 };
 template <int WORDS>

@@ -58,7 +58,7 @@ int grid_for(int64_t warps, int sm_count) {
 
 cudaError_t launch_w4_pack(int d_out, int d_in, int group, const void* W, uint8_t* codes,
                            void* scale, cudaStream_t st) {
-  const int ng = (d_in + group - 1) / group;
+  const int ng = w4_groups(d_in, group);
   w4_pack_kernel<<<grid_for((int64_t)d_out * ng, 148), 256, 0, st>>>(
       d_out, d_in, group, ng, static_cast<const bf*>(W), codes, static_cast<bf*>(scale));
   PKM_COUNT(1);
@@ -67,7 +67,7 @@ cudaError_t launch_w4_pack(int d_out, int d_in, int group, const void* W, uint8_
 
 cudaError_t launch_w4_unpack(int d_out, int d_in, int group, const W4Mat& W, void* out,
                              cudaStream_t st) {
-  const int ng = (d_in + group - 1) / group;
+  const int ng = w4_groups(d_in, group);
   w4_unpack_kernel<<<grid_for((int64_t)d_out * d_in / 64 + 1, 148), 256, 0, st>>>(
       d_out, d_in, group, ng, W.codes, W.scale, static_cast<bf*>(out));
   PKM_COUNT(1);

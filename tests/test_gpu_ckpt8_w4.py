@@ -245,3 +245,40 @@ def test_w4_block_in_a_graph_and_against_the_unpacked_block():
     move = (R.SLOPE * gm * (u.abs() + um * 2 ** -7) + a.abs() * um + a.abs() * u.abs()) * 2 ** -7.9
     bound = move @ flat["Wd"].double().abs().t() + 2.1 * want["y"][1]
     assert ((y.double() - y2.double()).abs() <= bound).all()
+
+
+# Each has the same power of two as its small twin, so that the kernels' columns per scale agree:
+# 32, 64 and 128 columns in one load.
+@pytest.mark.parametrize("group,twin", [(0x7fffffe0, 1632), (0x7fffffc0, 1728), (0x7fffff80, 1664)])
+def test_w4_groups_near_the_largest_integer_are_one_group_per_row(group, twin):
+    i, o = 1600, 100
+    W = rnd(2, o, i).bfloat16()
+    W[:, 0] *= torch.linspace(1, 9, o, device="cuda").bfloat16()  # a scale of its own for each row
+    want = P.alloc_w4(o, i, twin)
+    P.pkm_w4_pack(W, *want, group=twin)
+    assert (R.nibbles(want[0]) == R.pack4(W, twin)[0]).all() and want[1].unique().numel() > o // 2
+    codes, scale = P.alloc_w4(o + 1, i, group)
+    codes.fill_(99)
+    scale.fill_(5.0)
+    P.pkm_w4_pack(W, codes[:o], scale[:o], group=group)
+    assert torch.equal(codes[:o], want[0]) and torch.equal(scale[:o], want[1])
+    assert (codes[o] == 99).all() and (scale[o] == 5.0).all()
+    out, out2 = torch.empty_like(W), torch.empty_like(W)
+    P.pkm_w4_unpack(*want, out, group=group)
+    P.pkm_w4_unpack(*want, out2, group=twin)
+    assert torch.equal(out, out2)
+    for n, rows in ((1, o), (20, o), (20, 9600)):  # the last: the form for many rows
+        x = rnd(n, n, i).bfloat16()
+        q = want if rows == o else random_w4(4, rows, i, twin)
+        y, y2 = (torch.empty(n, rows, device="cuda") for _ in range(2))
+        P.pkm_w4_matvec(x, *q, y, group=group)
+        P.pkm_w4_matvec(x, *q, y2, group=twin)
+        assert torch.equal(y, y2)
+    f = 1472  # of one group too
+    packed = [random_w4(s, *shape, twin) for s, shape in enumerate(((f, i), (f, i), (o, f)))]
+    d = P.FfnDims(7, i, f, o)
+    ws, x = P.alloc_ffn_workspace(d, P.PKM_FWD), rnd(7, 7, i).bfloat16()
+    y, y2 = (torch.empty(7, o, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    P.pkm_w4_ffn(d, x, *packed, y, group=group, workspace=ws)
+    P.pkm_w4_ffn(d, x, *packed, y2, group=twin, workspace=ws)
+    assert torch.equal(y, y2)
