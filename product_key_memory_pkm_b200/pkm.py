@@ -572,6 +572,13 @@ class _Checked:
         return workspace.data_ptr(), workspace_bytes or workspace.nbytes
 
 
+def _int32(v: int, name: str, side: str = "") -> int:
+    """A size the library takes in 32 bits (of more, ctypes would pass the low bits)."""
+    if not -0x80000000 <= v <= 0x7fffffff:
+        raise ValueError(f"{name}{side}: {v} is beyond the library's integers")
+    return v
+
+
 @dataclass(frozen=True)
 class FfnDims:
     """Python mirror of ``pkm_ffn_dims``."""
@@ -584,6 +591,9 @@ class FfnDims:
 
     def __post_init__(self):
         s = pkm_ffn_dims(self.N, self.d_in, self.d_ff, self.d_out, self.act, self.flags)
+        for f, _ in s._fields_:  # ctypes cuts what does not fit to its low bits
+            if getattr(s, f) != getattr(self, f):
+                raise ValueError(f"{f}: {getattr(self, f)} is beyond the library's integers")
         object.__setattr__(self, "_c", s)  # the dims do not change: made once
 
     def c(self) -> pkm_ffn_dims:
@@ -687,7 +697,7 @@ def _ckpt8(ck: _Checked, values, name, codes, scale):
     if values.dim() != 2:
         raise ValueError(f"{name}: two dimensions wanted, got {values.dim()}")
     rows, cols = values.shape
-    runs = -(-cols // CKPT8_RUN)
+    runs = -(-_int32(cols, name, " columns") // CKPT8_RUN)
     return (rows, cols, PKM_F_FP32 if dt == f32 else 0, ck(values, name, dt, (rows, cols)),
             ck(codes, "codes", ck.torch.int8, (rows, runs * CKPT8_RUN)),
             ck(scale, "scale", f32, (rows, runs)))
@@ -719,8 +729,10 @@ def alloc_w4(d_out: int, d_in: int, group: int, device="cuda") -> tuple:
 
 
 def _w4(ck: _Checked, W, name: str, d_out: int, d_in: int, group: int) -> pkm_w4:
-    if group <= 0:
+    if _int32(group, "group") <= 0:
         raise ValueError(f"group: a positive multiple of 32 wanted, got {group}")
+    _int32(d_out, name, " rows")
+    _int32(d_in, name, " columns")
     codes, scale = W
     return pkm_w4(ck(codes, name, ck.torch.uint8, (d_out, d_in // 2)),
                   ck(scale, name, ck.torch.bfloat16, (d_out, -(-d_in // group))))

@@ -295,3 +295,59 @@ def test_kernels_that_wait_for_their_producer_take_no_restrict_pointers():
                 seen.append(re.findall(r"(\w+)\s*\(", head)[-1])
                 assert "__restrict__" not in head, seen[-1]
     assert seen == ["few_kernel", "small_jobs_kernel", "sum_parts_kernel"]
+
+
+def test_sizes_beyond_the_librarys_integers_are_refused(monkeypatch):
+    """ctypes passes the low bits of what does not fit: a group of 2^32 + 64 as 64, so that the
+    kernels would read more scales than the caller's tensor holds."""
+    for kw in (dict(N=1 << 64), dict(d_in=(1 << 32) + 64), dict(d_ff=(1 << 31)), dict(d_out=-1 << 32),
+               dict(act=1 << 32), dict(flags=1 << 32), dict(flags=-1)):
+        with pytest.raises(ValueError, match="beyond the library's integers"):
+            _d(**kw)
+
+    class Anywhere(P._Checked):
+        __slots__ = ()
+
+        def place(self, t, name):
+            pass
+
+        def stream(self, stream):
+            return None
+
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: calls.append(name) or P.PKM_OK
+
+    monkeypatch.setattr(P, "_Checked", Anywhere)
+    monkeypatch.setattr(P, "load", Library)
+    big = (1 << 32) + 64
+
+    def t(*shape, dtype=torch.bfloat16):  # no memory behind it
+        return torch.empty(*shape, dtype=dtype, device="meta")
+
+    def w4(o, i, group):
+        return P.alloc_w4(o, i, group, "meta")
+
+    d = _d(N=2, d_ff=96, d_out=64)
+    f32 = torch.float32
+    P.pkm_w4_matvec(t(2, 64), *w4(8, 64, 64), t(2, 8, dtype=f32))
+    assert calls == ["pkm_w4_matvec"]  # a call in range goes through
+    calls.clear()
+    for call in (
+            lambda: P.pkm_w4_matvec(t(2, 128), *w4(8, 128, big), t(2, 8, dtype=f32), group=big),
+            lambda: P.pkm_w4_matvec(t(2, big), *w4(8, big, 64), t(2, 8, dtype=f32)),
+            lambda: P.pkm_w4_matvec(t(2, 64), *w4(big, 64, 64), t(2, big, dtype=f32)),
+            lambda: P.pkm_w4_pack(t(8, 128), *w4(8, 128, big), group=big),
+            lambda: P.pkm_w4_pack(t(8, big), *w4(8, big, 64)),
+            lambda: P.pkm_w4_pack(t(big, 64), *w4(big, 64, 64)),
+            lambda: P.pkm_w4_unpack(*w4(8, 128, big), t(8, 128), group=big),
+            lambda: P.pkm_w4_unpack(*w4(big, 64, 64), t(big, 64)),
+            lambda: P.pkm_w4_ffn(d, t(2, 64), w4(96, 64, big), w4(96, 64, big), w4(64, 96, big),
+                                 t(2, 64), group=big),
+            lambda: P.pkm_ckpt8_pack(t(2, big), *P.alloc_ckpt8(2, big, "meta")),
+            lambda: P.pkm_ckpt8_unpack(*P.alloc_ckpt8(2, big, "meta"), t(2, big, dtype=f32))):
+        with pytest.raises(ValueError, match="beyond the library's integers"):
+            call()
+    assert not calls
