@@ -562,6 +562,8 @@ class _Checked:
         return _stream(stream)
 
     def workspace(self, workspace, workspace_bytes):
+        if workspace_bytes < 0:  # the largest size there is, as size_t
+            raise ValueError(f"workspace_bytes: {workspace_bytes}")
         if workspace is None or isinstance(workspace, int):
             return workspace, workspace_bytes
         if not workspace.is_contiguous():

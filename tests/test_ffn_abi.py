@@ -351,3 +351,17 @@ def test_sizes_beyond_the_librarys_integers_are_refused(monkeypatch):
         with pytest.raises(ValueError, match="beyond the library's integers"):
             call()
     assert not calls
+
+
+def test_negative_workspace_sizes_are_refused():
+    """size_t makes -1 the largest size there is: every workspace would look large enough."""
+    class Anywhere(P._Checked):
+        __slots__ = ()
+
+        def place(self, t, name):
+            pass
+
+    for ws in (torch.empty(256, dtype=torch.uint8), FAKE):
+        with pytest.raises(ValueError, match="workspace_bytes"):
+            Anywhere().workspace(ws, -1)
+    assert Anywhere().workspace(FAKE, 64) == (FAKE, 64)
