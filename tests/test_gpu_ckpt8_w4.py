@@ -282,3 +282,38 @@ def test_w4_groups_near_the_largest_integer_are_one_group_per_row(group, twin):
     P.pkm_w4_ffn(d, x, *packed, y, group=group, workspace=ws)
     P.pkm_w4_ffn(d, x, *packed, y2, group=twin, workspace=ws)
     assert torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("n,i,o", [(1, 64, 300), (5, 1600, 2048), (16, 8192, 700), (64, 1600, 515),
+                                   (12, 1600, 9600), (64, 4128, 9600)])
+def test_w4_sums_keep_their_bits(n, i, o, group):
+    """The 2-norm of a product's error.  An instruction adds 16 exact products to a sum, each of
+    the 17 cut at 2^-23 of the largest; with products of variance v the largest is about 4 sqrt(v),
+    so the i / 16 instructions of a row leave (i / 16) (17 / 3) 2^-46 16 v in the mean square, or
+    5.7 * 2^-46 of the result's i v; the i / 32 scaled additions leave i / 32 / 6 * 2^-48.  Twice the
+    root of the two covers the scales' spread."""
+    x = rnd(n + 1, n, i).bfloat16()
+    codes, scale = random_w4(i, o, i, group)
+    y = torch.empty(n, o, device="cuda")
+    P.pkm_w4_matvec(x, codes, scale, y, group=group)
+    want = x.double() @ R.values4(R.nibbles(codes), scale, group).t()
+    off = ((y.double() - want).norm() / want.norm()).item()
+    assert off <= 2 * 2.0 ** -23 * (5.7 + i / 768) ** 0.5
+
+
+@pytest.mark.parametrize("n,i,f,o,group", [(1, 96, 160, 50, 32), (8, 1600, 704, 333, 64),
+                                           (64, 640, 1056, 129, 96)])
+def test_w4_block_writes_nothing_outside_its_buffers(n, i, f, o, group):
+    packed = [random_w4(s, *shape, group) for s, shape in enumerate(((f, i), (f, i), (o, f)))]
+    x, d, edge = rnd(n, n, i).bfloat16(), P.FfnDims(n, i, f, o), 1024
+    need = P.pkm_ffn_workspace_bytes(d, P.PKM_FWD)
+    raws = [torch.full((k + 2 * edge,), 0xA5, dtype=torch.uint8, device="cuda") for k in (2 * n * o, need)]
+    y = raws[0][edge:edge + 2 * n * o].view(torch.bfloat16).view(n, o)
+    P.pkm_w4_ffn(d, x, *packed, y, group=group, workspace=raws[1][edge:edge + need],
+                 workspace_bytes=need)
+    for raw, k in zip(raws, (2 * n * o, need)):
+        assert (raw[:edge] == 0xA5).all() and (raw[edge + k:] == 0xA5).all()
+    y2 = torch.empty_like(y)
+    P.pkm_w4_ffn(d, x, *packed, y2, group=group, workspace=P.alloc_ffn_workspace(d, P.PKM_FWD))
+    assert torch.equal(y, y2)

@@ -489,3 +489,105 @@ def test_few_token_calls_back_to_back_read_their_own_inner_values(n, kind):
         call(xs[i & 1], got[i])
     for i in range(200):
         assert torch.equal(got[i], want[i & 1]), i
+
+
+class Fenced:
+    """Tensors that lie between two KiB of a known pattern; check() finds what wrote there."""
+    EDGE = 1024
+
+    def __init__(self):
+        self.raw = []
+
+    def __call__(self, shape, dtype, fill=None):
+        n = torch.empty(shape, dtype=dtype, device="meta").nbytes
+        raw = torch.full((n + 2 * self.EDGE,), 255, dtype=torch.uint8, device="cuda")
+        raw[:self.EDGE] = raw[self.EDGE + n:] = 0xA5
+        self.raw.append((raw, n))
+        t = raw[self.EDGE:self.EDGE + n].view(dtype).view(shape)
+        return t if fill is None else t.fill_(fill)
+
+    def like(self, t, fill=None):
+        return None if t is None else self(t.shape, t.dtype, fill)
+
+    def check(self):
+        for raw, n in self.raw:
+            assert (raw[:self.EDGE] == 0xA5).all() and (raw[self.EDGE + n:] == 0xA5).all(), n
+
+
+@pytest.mark.parametrize("mode", ["bf16", "bf16-ckpt8", "fp32", "fp32-ckpt8", "simt", "simt-ckpt8"])
+@pytest.mark.parametrize("size", [(1, 8, 8, 8), (3, 64, 40, 72), (65, 136, 264, 200),
+                                  (300, 328, 1000, 520), (40, 2048, 2048, 64), (513, 1024, 2056, 264),
+                                  (1100, 1032, 520, 264)])
+def test_nothing_is_written_outside_the_buffers(size, mode):
+    """Results, kept values, gradients and a workspace of exactly the stated size, each between
+    fences; what is inside has the same bits as without them."""
+    n, di, f, do = size
+    dtype = torch.float32 if mode.startswith("fp32") else torch.bfloat16
+    flags = (P.PKM_F_SIMT if mode.startswith("simt") else 0) | (
+        P.PKM_FFN_CKPT8 if mode.endswith("ckpt8") else 0)
+    t, dy = make(n, di, f, do, dtype, seed=n)
+    for grad16 in (0, P.PKM_FFN_GRAD_BF16)[:1 if dtype == torch.float32 else 2]:
+        d, fence = dims(n, di, f, do, dtype, "gelu", flags | grad16), Fenced()
+        wt = torch.bfloat16 if grad16 else torch.float32
+
+        def workspace(which):
+            need = P.pkm_ffn_workspace_bytes(d, which)
+            return dict(workspace=fence((need,), torch.uint8), workspace_bytes=need)
+
+        plain = dict(y=torch.empty_like(dy), none=torch.empty_like(dy), saved=P.alloc_ffn_saved(d),
+                     grads={"d" + k: torch.zeros_like(v, dtype=v.dtype if k == "x" else wt)
+                            for k, v in t.items()})
+        fenced = dict(y=fence.like(dy), none=fence.like(dy),
+                      saved={k: fence.like(v) for k, v in plain["saved"].items()},
+                      grads={k: fence.like(v, 0) for k, v in plain["grads"].items()})
+        for b, ws in ((plain, lambda w: dict(workspace=scratch(d, w))), (fenced, workspace)):
+            P.pkm_ffn_forward(d, **t, y=b["none"], **ws(P.PKM_FWD))
+            P.pkm_ffn_forward(d, **t, y=b["y"], saved=b["saved"], **ws(P.PKM_FWD))
+            P.pkm_ffn_backward(d, **t, saved=b["saved"], dy=dy, **b["grads"], **ws(P.PKM_BWD))
+        fence.check()
+        assert torch.equal(fenced["y"], plain["y"]) and torch.equal(fenced["none"], plain["none"])
+        for part in ("saved", "grads"):
+            for k, v in plain[part].items():
+                assert v is None or torch.equal(fenced[part][k], v), k
+    assert P.pkm_check_status() == P.PKM_OK
+
+
+def _norm_off(got, want):
+    return ((got.double() - want).norm() / want.norm()).item()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("ckpt8", [0, P.PKM_FFN_CKPT8])
+@pytest.mark.parametrize("size", [(64, 64, 256, 64), (130, 72, 520, 136), (515, 1600, 312, 1600),
+                                  (1100, 1032, 520, 264)])
+@pytest.mark.parametrize("store", ["fp32", "simt"])
+def test_everything_between_the_products_stays_in_32_bits(size, store, ckpt8, act):
+    """fp32 storage, and bf16 storage with PKM_F_SIMT, whose h, dg and du are fp32 too.
+
+    The 2-norm of an error.  Adding K terms of random sign rounds K times by at most 2^-24 of a
+    partial sum whose mean square grows evenly up to the result's, so the error is at most
+    sqrt(K / 6) 2^-24 of it.  With g of variance 1, the errors of g and u enter h at most 1.9 times
+    (the largest act' over the norm of act: 1.84 for SiLU, 1.73 for GELU) and once, together
+    sqrt(4.6 d_in / 6), below sqrt(d_in); the functions are good to 8 * 2^-24.  So y stays within
+    2^-24 sqrt(d_in + d_ff + 64), and the gradients, sums over d_out, 2 d_ff and the tokens of
+    factors that are read exactly, within 2^-24 sqrt(d_out + 2 d_ff + N + 64).  A loss of three or
+    four bits passes neither.  A result in bf16 is rounded once more, elementwise, by 2^-8 of its
+    value."""
+    n, di, f, do = size
+    dtype = torch.float32 if store == "fp32" else torch.bfloat16
+    once = 0.0 if store == "fp32" else 2.0 ** -8
+    d = dims(n, di, f, do, dtype, act, ckpt8 | (P.PKM_F_SIMT if store == "simt" else 0))
+    t, dy = make(n, di, f, do, dtype, seed=n + 1)
+    y, saved = torch.empty(n, do, dtype=dtype, device="cuda"), P.alloc_ffn_saved(d)
+    P.pkm_ffn_forward(d, **t, y=y, saved=saved, workspace=scratch(d, P.PKM_FWD))
+    value, bound = R.forward(act, **t, r=2.0 ** -24)["y"]
+    R.check(y, (value, bound + once * value.abs()), "y")
+    if store == "fp32":
+        assert _norm_off(y, value) <= 2.0 ** -24 * (di + f + 64) ** 0.5
+    out = run_backward(d, t, saved, dy)
+    want = R.backward(act, *t.values(), *values_of(d, saved), dy, 2.0 ** -24, 2.0 ** -23)
+    for k, v in out.items():
+        value, bound = want[k]
+        R.check(v, (value, bound + (once * value.abs() if k == "dx" else 0)), k)
+        if store == "fp32" or k != "dx":  # weight gradients are fp32
+            assert _norm_off(v, value) <= 2.0 ** -24 * (do + 2 * f + n + 64) ** 0.5, k
