@@ -571,8 +571,9 @@ def test_everything_between_the_products_stays_in_32_bits(size, store, ckpt8, ac
     sqrt(4.6 d_in / 6), below sqrt(d_in); the functions are good to 8 * 2^-24.  So y stays within
     2^-24 sqrt(d_in + d_ff + 64), and the gradients, sums over d_out, 2 d_ff and the tokens of
     factors that are read exactly, within 2^-24 sqrt(d_out + 2 d_ff + N + 64).  A loss of three or
-    four bits passes neither.  A result in bf16 is rounded once more, elementwise, by 2^-8 of its
-    value."""
+    four bits passes neither.  A result in bf16 is rounded once more, elementwise by 2^-8 of its
+    value and in the norm by 2^-8 / sqrt(3) = 2.26e-3 at most: evenly within the step, and no
+    significand is below 1.  (With h in bf16 as well it is 2.35e-3.)"""
     n, di, f, do = size
     dtype = torch.float32 if store == "fp32" else torch.bfloat16
     once = 0.0 if store == "fp32" else 2.0 ** -8
@@ -582,8 +583,8 @@ def test_everything_between_the_products_stays_in_32_bits(size, store, ckpt8, ac
     P.pkm_ffn_forward(d, **t, y=y, saved=saved, workspace=scratch(d, P.PKM_FWD))
     value, bound = R.forward(act, **t, r=2.0 ** -24)["y"]
     R.check(y, (value, bound + once * value.abs()), "y")
-    if store == "fp32":
-        assert _norm_off(y, value) <= 2.0 ** -24 * (di + f + 64) ** 0.5
+    limit = 2.0 ** -24 * (di + f + 64) ** 0.5
+    assert _norm_off(y, value) <= (limit if store == "fp32" else 2.0 ** -8 / 3 ** 0.5)
     out = run_backward(d, t, saved, dy)
     want = R.backward(act, *t.values(), *values_of(d, saved), dy, 2.0 ** -24, 2.0 ** -23)
     for k, v in out.items():
