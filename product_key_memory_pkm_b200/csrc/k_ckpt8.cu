@@ -7,7 +7,6 @@
 // pack 62 us (5.3 TB/s; it issues instructions in four of five cycles, about 110 per chunk, of
 // which the exact halves cost 3 per value).
 #include <type_traits>
-#include <type_traits>
 
 #include "ffn_internal.cuh"
 

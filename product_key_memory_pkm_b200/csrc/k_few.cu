@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(32 * kWideWarps, 1)
     wide_kernel(int N, W4Shape sh, int chunk, const bf* __restrict__ x, W4Mat W,
                 float* __restrict__ y) {
   using Unit = W4Unit<WORDS>;
-  constexpr int T = NT * 8, kIlp = NT < kWideIlp ? NT : kWideIlp;
+  constexpr int T = NT * 8, kIlp = kWideIlp;
   constexpr int kAhead = NT == 8 ? 1 : 2;  // units requested before their use, as registers allow
   extern __shared__ __align__(16) unsigned char xs[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -581,15 +581,21 @@ cudaError_t launch_m(int N, const typename Of::Shape& sh, const bf* x, const typ
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Two blocks of rows per tile where even so every SM gets several tiles.
+// Two blocks of rows per tile where even so every SM gets several tiles.  (For fp32 results of
+// more than 8 tokens that is where wide_form holds.)
 template <class Unit, class Of, int NT, Few OUT, int ACT>
 cudaError_t launch(int N, const typename Of::Shape& sh, const bf* x, const typename Of::Mat& W0,
                    const typename Of::Mat& W1, void* out, bool first, int sm_count,
                    cudaStream_t st) {
-  if (OUT == Few::kGate || (NT <= 2 && sh.d_out >= 2 * kRows * 4 * sm_count))
+  if constexpr (OUT == Few::kGate) {
     return launch_m<Unit, Of, 2, NT, OUT, ACT>(N, sh, x, W0, W1, out, first, sm_count, st);
-  return launch_m<Unit, Of, OUT == Few::kGate ? 2 : 1, NT, OUT, ACT>(N, sh, x, W0, W1, out, first,
-                                                                    sm_count, st);
+  } else {
+    if constexpr (NT == 1 || (NT == 2 && OUT == Few::kBf16)) {
+      if (sh.d_out >= 2 * kRows * 4 * sm_count)
+        return launch_m<Unit, Of, 2, NT, OUT, ACT>(N, sh, x, W0, W1, out, first, sm_count, st);
+    }
+    return launch_m<Unit, Of, 1, NT, OUT, ACT>(N, sh, x, W0, W1, out, first, sm_count, st);
+  }
 }
 
 template <class Unit, class Of, Few OUT, int ACT, int MAXT>
@@ -620,7 +626,6 @@ cudaError_t w4(int64_t N, int d_in, int d_out, int group, const bf* x, const W4M
 template <int WORDS>
 cudaError_t wide(int N, const W4Shape& sh, const bf* x, const W4Mat& W, float* y, int sm_count,
                  cudaStream_t st) {
-  if (N <= 8) return launch_wide<WORDS, 1>(N, sh, x, W, y, sm_count, st);
   if (N <= 16) return launch_wide<WORDS, 2>(N, sh, x, W, y, sm_count, st);
   return N <= 32 ? launch_wide<WORDS, 4>(N, sh, x, W, y, sm_count, st)
                  : launch_wide<WORDS, 8>(N, sh, x, W, y, sm_count, st);
