@@ -498,8 +498,8 @@ pkm_status pkm_w4_unpack(int32_t d_out, int32_t d_in, int32_t group, const pkm_w
 pkm_status pkm_w4_matvec(int64_t N, int32_t d_in, int32_t d_out, int32_t group, const void* x,
                          const pkm_w4* W, float* y, void* stream);
 /* The gated block with 4-bit weights: Wg, Wu [d_ff][d_in], Wd [d_out][d_ff]; x and y bf16,
- * d->flags == 0, d_ff a multiple of 32, any d_out, N <= PKM_W4_MAX_TOKENS.  Workspace:
- * pkm_ffn_workspace_bytes(d, PKM_FWD). */
+ * h rounded to bf16 before the second product (g and u stay fp32), d->flags == 0, d_ff a multiple
+ * of 32, any d_out, N <= PKM_W4_MAX_TOKENS.  Workspace: pkm_ffn_workspace_bytes(d, PKM_FWD). */
 pkm_status pkm_w4_ffn(const pkm_ffn_dims* d, int32_t group, const void* x, const pkm_w4* Wg,
                       const pkm_w4* Wu, const pkm_w4* Wd, void* y, void* workspace,
                       size_t workspace_bytes, void* stream);

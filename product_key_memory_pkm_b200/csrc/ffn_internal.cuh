@@ -202,7 +202,10 @@ cudaError_t launch_w4_matvec(int64_t N, int d_in, int d_out, int group, const vo
                              const W4Mat& W, float* y, int sm_count, cudaStream_t st);
 cudaError_t launch_w4_ffn(const FfnPlan& p, int group, const void* x, const W4Mat& Wg,
                           const W4Mat& Wu, const W4Mat& Wd, void* y, void* ws, cudaStream_t st);
-// The forward of a few tokens with nothing kept (bf16 weights).  ws: h [N][d_ff] bf16.
+// The forward of a few tokens with nothing kept (bf16 weights).  ws: h [N][d_ff] bf16.  Up to 16:
+// on the device, this against the CTA-pair engine, us, 1600 x 6400 x 1600: 8 tokens 12.6 / 33.3,
+// 16 tokens 18.1 / 29.3, 17 tokens 31.6 / 33.8, 32 tokens 31.8 / 29.7, 64 tokens 69.9 / 30.3.
+// (Narrower blocks cross later: 1024 x 2728 x 1024 at 32 tokens 13.4 / 24.8, at 64 29.4 / 25.0.)
 constexpr int64_t kFfnFewTokens = 16;
 cudaError_t launch_ffn_few(const FfnPlan& p, const void* x, const void* Wg, const void* Wu,
                            const void* Wd, void* y, void* ws, cudaStream_t st);

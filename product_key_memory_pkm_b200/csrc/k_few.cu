@@ -229,7 +229,8 @@ enum class Few { kF32, kBf16, kGate };  // y fp32, y bf16, or h = act(first) * s
 // both), or for the gate one of each matrix.
 // Units a warp has in flight, and the CTAs an SM holds: few units and several CTAs, so that
 // the CTAs of one grid are resident together and none waits for another's last loads (one
-// token, 1600 x 6400 x 1600 in bf16: 18 us; two units and 2 CTAs 24, four units and 1 CTA 32).
+// token, 1600 x 6400 x 1600 in bf16, whole calls: 18 us, on the device 14.4; whole calls with two
+// units and 2 CTAs 24, with four units and 1 CTA 32).
 template <class Unit, int M, int NT>
 struct Depth {  // 4-bit: 8 words per row and matrix in flight, 4 for the two of a gate
   static constexpr int wide = 8 / M / Unit::kWords;
@@ -401,9 +402,11 @@ __global__ void __launch_bounds__(kTpb, Depth<Unit, M, NT>::ctas)
 // shared memory and each of its warps takes 16 rows through all of k.  Rows are dealt so that they
 // fill whole rounds of the SMs with as many warps as fit, up to 24: a warp's products depend on
 // one another, and other warps and kWideIlp products at a time fill the gaps.  Against 50264 x
-// 1600: 24 us for 16 tokens (few_kernel 39), 33 for 32 (89), 55 for 64 (140); for 8 tokens both
-// take 20 to 24, so those stay there.  Still bound by the latency of that chain and of the reads
-// of x: the weights alone would take 6.6 us, issuing all products about 20.
+// 1600, whole calls: 24 us for 16 tokens (few_kernel 39), 33 for 32 (89), 55 for 64 (140; on the
+// device 48 with the weights in L2, 53 from HBM); for 8 tokens both take 20 to 24, so those stay
+// there.  The weights alone would take 6.6 us.  At 64 tokens instructions issue in 51 % of the
+// cycles, the tensor pipe works in 38 %, and every 16 rows' reading of x keeps the shared-memory
+// port busy for 41 %; the rest is the latency of a warp's chain.
 constexpr int kWideRows = 16, kWideWarps = 24, kWideIlp = 2;
 constexpr int kWideSmem = 225 * 1024;
 
@@ -534,7 +537,14 @@ cudaError_t launch_wide(int N, const W4Shape& sh, const bf* x, const W4Mat& W, f
   return cudaGetLastError();
 }
 
-// Rows enough that every SM has several warps.
+// Rows enough that every SM has several warps.  1600 columns, few_kernel against this, us on the
+// device:                  9 tokens     16 tokens    32 tokens    64 tokens
+//    7104 rows         5.5   9.3    5.7   9.7   10.6  15.2   18.3  30.3
+//    9472 (the limit)  8.1   8.9    8.4   9.3   11.0  14.5   23.9  29.3
+//   12000              9.2  10.6    9.4  11.1   15.0  16.4   34.8  31.2
+//   18944             13.0  10.6   13.2  10.9   19.8  16.2   45.9  31.8
+//   33333             20.5  15.1   20.9  15.6   35.7  22.0   84.4  38.3
+// They cross between 9472 and 18944 rows, so near the limit this is up to a third slower.
 bool wide_form(int64_t N, int d_out, int sm_count) {
   return N > 8 && d_out >= 4 * kWideRows * sm_count;
 }

@@ -1,4 +1,7 @@
-// 4-bit weights: packing a bf16 matrix and unpacking it.  Done once per matrix; bound by HBM.
+// 4-bit weights: packing a bf16 matrix (once per matrix) and unpacking it (once per prompt of more
+// tokens than the products take).  Bound by instructions, not by HBM: 50264 x 1600 takes 285 us to
+// pack and 143 to unpack where the bytes would take 31; they issue in 71 and 63 % of the cycles, on
+// a division per value and a 64-bit division per byte, with 2-byte accesses.
 #include <algorithm>
 
 #include "ffn_internal.cuh"

@@ -509,7 +509,8 @@ def pkm_shard_scatter_dw(dims: Dims, perm, dw_ret, dw, stream=None) -> None:
 
 # ------------------------------------------------------- gated feed-forward block
 # Unlike the raw-address calls above, these check the tensors they are given: type, shape,
-# contiguity and device (integer addresses pass unchecked).
+# contiguity and device.  (An integer address passes unchecked; not for a tensor that gives the
+# call its sizes, as the checkpoints' values and the 4-bit products' x and codes do.)
 
 _torch = None
 
