@@ -47,10 +47,11 @@ constexpr uint32_t kInfBits = 0x7f800000u;
 // quotient top / 127 comes from the rounded 1 / 127 and one exact remainder, which gives the
 // correctly rounded result for every fp32 mantissa (all 2^23 tried).  inv is correctly rounded or,
 // for values exact in bf16 (BF16), whose codes tolerate it, off by up to 3 of its last places.
-// Runs outside 1e-30 .. 1e37, where one of the steps could leave the normal numbers, divide.
+// Runs outside 1e-30 .. 2e36, where one of the steps could leave the normal numbers (127 a among
+// them), divide.
 struct CkptScale {
   float scale, inv, top;
-  __device__ bool plain() const { return top >= 1e-30f && top <= 1e37f; }
+  __device__ bool plain() const { return top >= 1e-30f && top <= 2e36f; }
 };
 template <bool BF16>
 __device__ __forceinline__ CkptScale ckpt_scale(uint32_t top_bits) {

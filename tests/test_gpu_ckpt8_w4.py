@@ -317,3 +317,23 @@ def test_w4_block_writes_nothing_outside_its_buffers(n, i, f, o, group):
     y2 = torch.empty_like(y)
     P.pkm_w4_ffn(d, x, *packed, y2, group=group, workspace=P.alloc_ffn_workspace(d, P.PKM_FWD))
     assert torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_checkpoint_halves_at_every_magnitude(dtype):
+    """Runs from 1e-36 to 3e38 that hold their largest value's half (63.5 steps), its neighbours and
+    other halves: the codes are those of 64 bits wherever 127 a still is a number and beyond."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    top = 10.0 ** torch.linspace(-36, 38.4, 6000, device="cuda", dtype=torch.float64)
+    top = (top * (1 + torch.rand(6000, device="cuda", generator=gen, dtype=torch.float64))).clamp(max=3.3e38)
+    top = top.to(dtype).float()
+    odd = torch.randint(0, 127, (6000, 28), device="cuda", generator=gen) * 2 + 1
+    v = (top.double()[:, None] * odd / 254).to(dtype).float()      # halves, to within a rounding
+    half = (top / 2)[:, None]
+    near = [torch.nextafter(half, half * s) for s in (0.5, 2.0)]
+    x = torch.cat([top[:, None], half, *near, v], 1)
+    x = (x * torch.where(torch.rand(x.shape, device="cuda", generator=gen) < 0.5, -1.0, 1.0)).to(dtype)
+    codes, scale = pack(x)
+    wc, ws = R.pack8(x)
+    assert torch.equal(scale, ws)
+    assert torch.equal(codes, wc)
