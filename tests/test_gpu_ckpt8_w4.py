@@ -337,3 +337,26 @@ def test_checkpoint_halves_at_every_magnitude(dtype):
     wc, ws = R.pack8(x)
     assert torch.equal(scale, ws)
     assert torch.equal(codes, wc)
+
+
+@pytest.mark.parametrize("o", [300, 9600])
+def test_w4_sums_depend_on_the_other_tokens_by_their_order_only(o):
+    """A token's results have the same bits in calls of the same blocks of 8 tokens, whatever else
+    is in the call, and between such groups differ by no more than two fp32 sums may."""
+    i, group = 1600, 64
+    x = rnd(6, 64, i).bfloat16()
+    codes, scale = random_w4(3, o, i, group)
+    W = R.values4(R.nibbles(codes), scale, group)
+    bound = 2 * (i + 8) * R.E32 * (x.double().abs() @ W.abs().t())
+    whole = torch.empty(64, o, device="cuda")
+    P.pkm_w4_matvec(x, codes, scale, whole, group=group)
+    for sizes in ((8, 1, 5), (16, 9, 13), (32, 17, 30), (64, 33, 50)):
+        first = torch.empty(sizes[0], o, device="cuda")
+        P.pkm_w4_matvec(x[:sizes[0]], codes, scale, first, group=group)
+        assert ((first.double() - whole[:sizes[0]]).abs() <= bound[:sizes[0]]).all()
+        for n in sizes[1:]:
+            xs = x[:n].clone()
+            xs[1:] = -xs[1:] * 3  # other tokens beside the first
+            y = torch.empty(n, o, device="cuda")
+            P.pkm_w4_matvec(xs, codes, scale, y, group=group)
+            assert torch.equal(y[0], first[0])
